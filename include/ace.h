@@ -441,6 +441,158 @@ ACE_API size_t ace_tau_workspace_size(void);
 ACE_API ace_status ace_tau_quantile(const float* score, int n_tok, int k, int64_t n_skip,
                                     float* tau, void* ws, size_t ws_bytes, void* stream);
 
+/* ========================================================================
+ * The 8-bit layer: operators around experts whose weights and inputs are
+ * 8-bit integers with a scale for each output channel and each row.  The
+ * pages describe bf16 experts; these are the same layer's steps for
+ * checkpoints stored in 8 bits, and for routers with sigmoid scores, a
+ * balance bias or groups of experts.  Used one after the other they make the
+ * layer (token_dynamic_expert_b200/layer_i8.py):
+ *     ace_add_rmsnorm -> router logits -> ace_gate_topk -> ace_moe_group ->
+ *     ace_matmul_i8 (gate and up) -> ace_swiglu -> ace_matmul_i8 (down) ->
+ *     ace_moe_combine
+ * Every call is asynchronous, allocates nothing and can be captured.  Row
+ * strides (ld*) are in elements.  Outputs overlap no input and no other
+ * output except where stated; an overlap that the host can see is
+ * ACE_ERR_INVALID_ARG.
+ * ===================================================================== */
+
+/* ------------------------------------------------------------------------
+ * ace_add_rmsnorm -- residual addition, RMSNorm and an int8 copy of its
+ *   result, in one pass over the rows:
+ *     s_t = round(x_t + residual_t)   (x_t itself without a residual)
+ *     r_t = 1 / sqrt(mean_j s_tj^2 + eps)
+ *     y_t = round(s_t r_t gamma)      (s_t r_t in fp32 first, then gamma)
+ *     M_t = max_j |s_tj gamma_j|,  q_tj = nearest int of 127 s_tj gamma_j / M_t
+ *     q_scale_t = M_t r_t / 127
+ *   so q q_scale stands for s r gamma before its rounding.  q is the correctly
+ *   rounded quotient (halves to even), |q| <= 127.  Sums are fp32; s and y are
+ *   rounded once to dtype.
+ *   x, residual, sum, y (device) [T][d] dtype, aligned to their element;
+ *   residual, sum, y and q may each be NULL (one output at least); gamma
+ *   (device) [d] fp32; q (device) [T][d] int8 with q_scale (device) [T] fp32.
+ *   sum and y may be x or residual themselves (same pointer and stride).
+ *   1 <= d <= 16384 (ACE_ERR_UNSUPPORTED above), any T >= 0, eps >= 0.  Rows
+ *   that start on 16-byte boundaries and a d that is a multiple of 16 bytes
+ *   move in 16-byte vectors; every other case is served, more slowly.
+ *   A row whose sum of squares or M is not finite in fp32 gets q = 0 and
+ *   q_scale = NaN; a row with M < 2^-126 gets q = 0 and q_scale = 0.
+ * ---------------------------------------------------------------------- */
+ACE_API ace_status ace_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                   int T, int d, ace_dtype dtype, const float* gamma, float eps,
+                                   void* sum, int64_t lds, void* y, int64_t ldy, int8_t* q,
+                                   int64_t ldq, float* q_scale, void* stream);
+
+/* Scores of ace_gate_topk, and what a group of experts is judged by. */
+typedef enum { ACE_SCORE_SOFTMAX = 0, ACE_SCORE_SIGMOID = 1 } ace_score;
+typedef enum { ACE_GROUP_MAX = 0, ACE_GROUP_TOP2 = 1 } ace_group_score;
+
+typedef struct {
+  ace_score score;
+  int n_groups;                /* E / n_groups neighbouring experts a group;
+                                  1 <= n_groups <= 32, dividing E          */
+  int topk_groups;             /* groups whose experts may be chosen       */
+  ace_group_score group_score; /* the group's largest choice value, or the
+                                  sum of its two largest                   */
+  int renorm_topk;             /* 1: weights divided by the chosen scores'
+                                  sum; 0: the scores themselves            */
+  float scale;                 /* factor on every weight, > 0              */
+  float tau;                   /* skip threshold of keep                   */
+} ace_gate_opts;
+
+/* ------------------------------------------------------------------------
+ * ace_gate_topk -- experts and weights of every token from its logits l:
+ *     s_e = softmax(l)_e or 1 / (1 + exp(-l_e))
+ *     c_e = s_e + bias_e; without a bias experts compare by l_e (same order)
+ *     the topk_groups best groups, then the k best experts in them, in order
+ *     (ties, of groups and of experts: the lower index)
+ *     weight_i = scale s_i, divided by the sum of the k chosen s if renorm
+ *     keep_i = 1 for the token's largest weight (ties: the first), else
+ *              !(weight_i factor[e_i] < tau)   (ACE's skip rule on weights)
+ *   The choice is that of exact arithmetic on the given logits and bias:
+ *   scores too close for fp32 are compared in fp64.  A weight's relative
+ *   error is a few fp32 roundings.
+ *   logits (device) [T][E] dtype, row stride ld; bias (device) [E] fp32 or
+ *   NULL; idx (device) [T][k] int32; weight (device) [T][k] fp32; factor
+ *   (device) [E] fp32 or NULL (1; the layer's amax or another ACE table);
+ *   keep (device) [T][k] uint8 or NULL.  1 <= E <= 512, 1 <= k <= 16, k at
+ *   most the experts of topk_groups groups.
+ *   A logit of -infinity is an expert out of service: score 0 (it is chosen
+ *   only when nothing better is left, or by its bias).  A token whose
+ *   chosen scores sum to 0 gets weights 0.  NaN compares above +infinity and
+ *   makes the token's weights NaN.
+ * ---------------------------------------------------------------------- */
+ACE_API ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype, int T, int E,
+                                 int k, const float* bias, const ace_gate_opts* opts, int32_t* idx,
+                                 float* weight, const float* factor, uint8_t* keep, void* stream);
+
+/* ------------------------------------------------------------------------
+ * ace_moe_group -- the kept slots in the order (expert, token, rank), as
+ *   ace_matmul_i8 and ace_moe_combine take them:
+ *     offsets [E + 1]   first position of each expert; offsets[E] = kept slots
+ *     slot_of [T][k]    a slot's position, -1 for a skipped one
+ *     slot_token [T k]  token of each position, or NULL
+ *     slot_gate [T k]   gate of each position (needs gate), or NULL
+ *   all int32 / fp32 device arrays; positions from offsets[E] on are left as
+ *   they were.  idx (device) [T][k] int32, keep (device) [T][k] uint8 or
+ *   NULL (all kept), gate (device) [T][k] fp32.  An idx outside 0 .. E - 1
+ *   counts as skipped.  E <= 512, k <= 16, T k < 2^31.  Deterministic.
+ * ---------------------------------------------------------------------- */
+ACE_API ace_status ace_moe_group(const int32_t* idx, const uint8_t* keep, const float* gate,
+                                 int T, int k, int E, int32_t* offsets, int32_t* slot_of,
+                                 int32_t* slot_token, float* slot_gate, void* stream);
+
+/* Operands of ace_matmul_i8 (all pointers device). */
+typedef struct {
+  const int8_t* xq;        /* [n_rows][K], row stride ldx bytes              */
+  int64_t ldx;             /* a multiple of 16                               */
+  int n_rows;
+  const float* x_scale;    /* [n_rows]                                       */
+  const int8_t* wq;        /* [E][N][K]                                      */
+  const float* w_scale;    /* [E][N]                                         */
+  int E, N, K;
+  const int32_t* offsets;  /* [E + 1] first slot of each expert, or NULL:
+                              one matrix (E = 1) for every slot              */
+  const int32_t* row_of;   /* [S] row of xq of each slot, or NULL: its own   */
+  const float* slot_scale; /* [S] factor on the slot's outputs (its gate), or
+                              NULL                                           */
+} ace_i8_product;
+
+/* ------------------------------------------------------------------------
+ * ace_matmul_i8 -- product of 8-bit integer matrices with a scale for each
+ *   row and each output channel, dense or grouped by expert:
+ *     out[s][n] = slot_scale[s] x_scale[r] w_scale[e][n]
+ *                 sum_k xq[r][k] wq[e][n][k],   r = row_of[s],
+ *     for offsets[e] <= s < offsets[e + 1]
+ *   The sum is exact in int32; it is rounded to fp32, scaled in fp32 and
+ *   rounded once to out_dtype.
+ *   S: rows of out (device) [S][N] out_dtype, row stride ldo, aligned to its
+ *   element.  offsets rise from 0 to at most S; rows of out from offsets[E] on
+ *   are left as they were (their number may be known to the device alone).
+ *   Offsets that do not raise ACE_FLAG_BAD_INDEX and nothing is computed.  A
+ *   row_of outside 0 .. n_rows - 1 gives a row of zeros.  xq and wq 16-byte
+ *   aligned, K a multiple of 16 up to 65536, E <= 512, any N >= 1.
+ *   ws: at least 256 bytes, its status word (ace_read_status).
+ * ---------------------------------------------------------------------- */
+ACE_API ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int64_t ldo,
+                                 ace_dtype out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * ace_swiglu -- h = SiLU(g) u of rows [g | u], with an int8 copy:
+ *     h_j = g_j / (1 + exp(-g_j)) u_j,  M = max_j |h_j|,
+ *     q_j = nearest int of 127 h_j / M,  q_scale = M / 127
+ *   q as in ace_add_rmsnorm (correctly rounded; rows that are not finite and
+ *   rows of zeros likewise); y = h rounded to dtype.
+ *   gu (device) [S][2 m] dtype; y (device) [S][m] dtype or NULL; q (device)
+ *   [S][m] int8 or NULL, with q_scale (device) [S] fp32 (y or q is given).
+ *   n_valid (device, one int32) or NULL: rows from *n_valid on are not read
+ *   and their outputs left as they were (ace_moe_group's offsets + E).
+ *   1 <= m <= 16384.
+ * ---------------------------------------------------------------------- */
+ACE_API ace_status ace_swiglu(const void* gu, int64_t ldgu, int S, int m, ace_dtype dtype,
+                              const int32_t* n_valid, void* y, int64_t ldy, int8_t* q,
+                              int64_t ldq, float* q_scale, void* stream);
+
 /* ------------------------------------------------------------------------
  * ace_read_status -- synchronise `stream` and return the device status
  *   word that the most recent call using `ws` left there (ACE_FLAG_* bits in

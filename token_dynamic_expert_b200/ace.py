@@ -5,6 +5,7 @@ current CUDA stream; every step of the computation runs in libace's kernels.
 There is no fallback: if ``libace.so`` is missing or fails to load, importing
 this module raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -26,6 +27,10 @@ ACE_GSP_FRO, ACE_GSP_SPECTRAL = 0, 1
 ACE_FUSE_MAX, ACE_FUSE_MIN, ACE_FUSE_MEAN, ACE_FUSE_GSP, ACE_FUSE_RCR = 0, 1, 2, 3, 4
 FUSIONS = {"max": ACE_FUSE_MAX, "min": ACE_FUSE_MIN, "mean": ACE_FUSE_MEAN, "gsp": ACE_FUSE_GSP,
            "rcr": ACE_FUSE_RCR}
+ACE_SCORE_SOFTMAX, ACE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": ACE_SCORE_SOFTMAX, "sigmoid": ACE_SCORE_SIGMOID}
+ACE_GROUP_MAX, ACE_GROUP_TOP2 = 0, 1
+GROUP_SCORES = {"max": ACE_GROUP_MAX, "top2": ACE_GROUP_TOP2}
 ACE_FLAG_BAD_INDEX, ACE_FLAG_TIMEOUT, ACE_FLAG_OVERFLOW = 0x1, 0x2, 0x4
 
 _vp = ctypes.c_void_p
@@ -48,6 +53,18 @@ class ace_debug_out(ctypes.Structure):
                 ("expert_offsets", _vp), ("slot_token", _vp), ("slot_rank", _vp),
                 ("n_kept", _vp), ("logits", _vp), ("ev_experts_begin", _vp),
                 ("ev_experts_mid", _vp), ("ev_experts_end", _vp), ("trace", _vp)]
+
+
+class ace_gate_opts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("renorm_topk", ctypes.c_int),
+                ("scale", ctypes.c_float), ("tau", ctypes.c_float)]
+
+
+class ace_i8_product(ctypes.Structure):
+    _fields_ = [("xq", _vp), ("ldx", ctypes.c_int64), ("n_rows", ctypes.c_int), ("x_scale", _vp),
+                ("wq", _vp), ("w_scale", _vp), ("E", ctypes.c_int), ("N", ctypes.c_int),
+                ("K", ctypes.c_int), ("offsets", _vp), ("row_of", _vp), ("slot_scale", _vp)]
 
 
 class ace_table_opts(ctypes.Structure):
@@ -100,6 +117,22 @@ _lib.ace_tau_workspace_size.restype = ctypes.c_size_t
 _lib.ace_tau_quantile.argtypes = [_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, _vp, _vp,
                                   ctypes.c_size_t, _vp]
 _lib.ace_tau_quantile.restype = ctypes.c_int
+_i64 = ctypes.c_int64
+_lib.ace_add_rmsnorm.argtypes = [_vp, _i64, _vp, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                 _vp, ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
+_lib.ace_add_rmsnorm.restype = ctypes.c_int
+_lib.ace_gate_topk.argtypes = [_vp, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                               _vp, _P(ace_gate_opts), _vp, _vp, _vp, _vp, _vp]
+_lib.ace_gate_topk.restype = ctypes.c_int
+_lib.ace_moe_group.argtypes = [_vp, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp,
+                               _vp, _vp, _vp]
+_lib.ace_moe_group.restype = ctypes.c_int
+_lib.ace_matmul_i8.argtypes = [_P(ace_i8_product), ctypes.c_int, _vp, _i64, ctypes.c_int, _vp,
+                               ctypes.c_size_t, _vp]
+_lib.ace_matmul_i8.restype = ctypes.c_int
+_lib.ace_swiglu.argtypes = [_vp, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp, _i64,
+                            _vp, _i64, _vp, _vp]
+_lib.ace_swiglu.restype = ctypes.c_int
 _lib.ace_noalloc_read_status.argtypes = [_P(ctypes.c_uint32), _vp]
 _lib.ace_noalloc_read_status.restype = ctypes.c_int
 _lib.ace_set_peer_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -258,6 +291,163 @@ def ace_moe_combine(slot_of, yslot, y, ws, stream=None):
                                 _stream(stream))
     _check(code, "ace_moe_combine")
     return y
+
+
+def _arg(t, name, dtype, shape):
+    """The pointer of an optional tensor argument, after its checks: dtype,
+    shape and C-contiguity."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, is %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return _ptr(t)
+
+
+def _rows(t, name, dtype, shape):
+    """(pointer, row stride) of an optional [rows][n] tensor whose rows may lie
+    apart; elements of a row are neighbours."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, is %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
+    n = t.shape[1]
+    if (n > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < n):
+        raise ValueError("%s must have rows of neighbouring elements" % name)
+    return _ptr(t), (t.stride(0) if t.shape[0] > 1 else n)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on_device(*tensors):
+    """A context with the tensors' device as the current one: the library
+    launches on the current device, and the default stream is that device's."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("tensors must be on a CUDA device, are on %s" % t.device)
+            if dev is not None and d != dev:
+                raise ValueError("tensors are on several devices: %d and %d" % (dev, d))
+            dev = d
+    return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def ace_add_rmsnorm(x, gamma, residual=None, sum=None, y=None, q=None, q_scale=None, eps=1e-6,
+                    stream=None):
+    """sum = x + residual, y = RMSNorm(sum) gamma, and its int8 rows q with
+    scales q_scale, whichever outputs are given (see include/ace.h).  x,
+    residual, sum, y [T][d]; q [T][d] int8; q_scale [T] fp32; rows may be
+    strided."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T][d]")
+    T, d = x.shape
+    dt = _dtype_code(x)
+    px, ldx = _rows(x, "x", x.dtype, (T, d))
+    pr, ldr = _rows(residual, "residual", x.dtype, (T, d))
+    ps, lds = _rows(sum, "sum", x.dtype, (T, d))
+    py, ldy = _rows(y, "y", x.dtype, (T, d))
+    pq, ldq = _rows(q, "q", torch.int8, (T, d))
+    pg, pqs = _arg(gamma, "gamma", torch.float32, (d,)), _arg(q_scale, "q_scale", torch.float32, (T,))
+    with _on_device(x, gamma, residual, sum, y, q, q_scale):
+        code = _lib.ace_add_rmsnorm(px, ldx, pr, ldr, T, d, dt, pg, float(eps), ps, lds,
+                                    py, ldy, pq, ldq, pqs, _stream(stream))
+    _check(code, "ace_add_rmsnorm")
+
+
+def ace_gate_topk(logits, idx, weight, bias=None, score="softmax", n_groups=1, topk_groups=1,
+                  group_score="max", renorm=True, scale=1.0, factor=None, tau=0.0, keep=None,
+                  stream=None):
+    """Experts idx [T][k] int32 and weights [T][k] fp32 of logits [T][E] (fp32
+    or bf16), and the skip mask keep [T][k] uint8 if given (see
+    include/ace.h)."""
+    if logits.dim() != 2 or idx.dim() != 2:
+        raise ValueError("logits must be [T][E] and idx [T][k]")
+    T, E = logits.shape
+    k = idx.shape[1]
+    pl, ld = _rows(logits, "logits", logits.dtype, (T, E))
+    opts = ace_gate_opts(score=SCORES[score], n_groups=int(n_groups), topk_groups=int(topk_groups),
+                         group_score=GROUP_SCORES[group_score], renorm_topk=int(bool(renorm)),
+                         scale=float(scale), tau=float(tau))
+    args = (pl, ld, _dtype_code(logits), T, E, k, _arg(bias, "bias", torch.float32, (E,)),
+            ctypes.byref(opts), _arg(idx, "idx", torch.int32, (T, k)),
+            _arg(weight, "weight", torch.float32, (T, k)), _arg(factor, "factor", torch.float32, (E,)),
+            _arg(keep, "keep", torch.uint8, (T, k)))
+    with _on_device(logits, idx, weight, bias, factor, keep):
+        code = _lib.ace_gate_topk(*args, _stream(stream))
+    _check(code, "ace_gate_topk")
+    return idx, weight
+
+
+def ace_moe_group(idx, E, offsets, slot_of, keep=None, gate=None, slot_token=None, slot_gate=None,
+                  stream=None):
+    """The kept slots of idx [T][k] in expert order: offsets [E + 1] and
+    slot_of [T][k], and slot_token / slot_gate [T * k] if given (see
+    include/ace.h)."""
+    if idx.dim() != 2:
+        raise ValueError("idx must be [T][k]")
+    T, k = idx.shape
+    E = int(E)
+    args = (_arg(idx, "idx", torch.int32, (T, k)), _arg(keep, "keep", torch.uint8, (T, k)),
+            _arg(gate, "gate", torch.float32, (T, k)), T, k, E,
+            _arg(offsets, "offsets", torch.int32, (E + 1,)), _arg(slot_of, "slot_of", torch.int32, (T, k)),
+            _arg(slot_token, "slot_token", torch.int32, (T * k,)),
+            _arg(slot_gate, "slot_gate", torch.float32, (T * k,)))
+    with _on_device(idx, offsets, slot_of, keep, gate, slot_token, slot_gate):
+        code = _lib.ace_moe_group(*args, _stream(stream))
+    _check(code, "ace_moe_group")
+    return offsets, slot_of
+
+
+def ace_matmul_i8(xq, x_scale, wq, w_scale, out, ws, offsets=None, row_of=None, slot_scale=None,
+                  stream=None):
+    """out [S][N] (bf16 or fp32) = scaled int8 product of xq [n][K] with
+    wq [N][K], or with wq [E][N][K] by the slots' experts (offsets [E + 1]);
+    row_of [S] reads the slots' rows of xq (see include/ace.h)."""
+    if xq.dim() != 2 or out.dim() != 2 or wq.dim() not in (2, 3):
+        raise ValueError("xq must be [n][K], wq [N][K] or [E][N][K], out [S][N]")
+    if wq.dim() == 3 and wq.shape[0] != 1 and offsets is None:
+        raise ValueError("wq of several experts needs offsets")
+    E = wq.shape[0] if wq.dim() == 3 else 1
+    N, K = wq.shape[-2:]
+    n, S = xq.shape[0], out.shape[0]
+    px, ldx = _rows(xq, "xq", torch.int8, (n, K))
+    po, ldo = _rows(out, "out", out.dtype, (S, N))
+    p = ace_i8_product(xq=px, ldx=ldx, n_rows=n, x_scale=_arg(x_scale, "x_scale", torch.float32, (n,)),
+                       wq=_arg(wq, "wq", torch.int8, wq.shape),
+                       w_scale=_arg(w_scale, "w_scale", torch.float32, wq.shape[:-1]), E=E, N=N, K=K,
+                       offsets=_arg(offsets, "offsets", torch.int32, (E + 1,)),
+                       row_of=_arg(row_of, "row_of", torch.int32, (S,)),
+                       slot_scale=_arg(slot_scale, "slot_scale", torch.float32, (S,)))
+    args = (ctypes.byref(p), S, po, ldo, _dtype_code(out), _ptr(ws), ws.numel())
+    with _on_device(xq, x_scale, wq, w_scale, out, ws, offsets, row_of, slot_scale):
+        code = _lib.ace_matmul_i8(*args, _stream(stream))
+    _check(code, "ace_matmul_i8")
+    return out
+
+
+def ace_swiglu(gu, y=None, q=None, q_scale=None, n_valid=None, stream=None):
+    """h = SiLU(g) u of rows gu [S][2 m] = [g | u]: y [S][m] and / or its int8
+    rows q [S][m] with scales q_scale [S]; rows from n_valid[0] on (int32,
+    device) are left alone (see include/ace.h)."""
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError("gu must be [S][2 m]")
+    S, m = gu.shape[0], gu.shape[1] // 2
+    pgu, ldgu = _rows(gu, "gu", gu.dtype, (S, 2 * m))
+    py, ldy = _rows(y, "y", gu.dtype, (S, m))
+    pq, ldq = _rows(q, "q", torch.int8, (S, m))
+    args = (pgu, ldgu, S, m, _dtype_code(gu), _arg(n_valid, "n_valid", torch.int32, (1,)), py, ldy, pq,
+            ldq, _arg(q_scale, "q_scale", torch.float32, (S,)))
+    with _on_device(gu, y, q, q_scale, n_valid):
+        code = _lib.ace_swiglu(*args, _stream(stream))
+    _check(code, "ace_swiglu")
 
 
 def _host_f32(t):

@@ -129,6 +129,11 @@ ace_status validate_layer(const ace_layer* L, bool need_experts) {
   return check_layer(L, need_experts);
 }
 uint64_t peer_wait_ns() { return g_peer_wait_ns.load(std::memory_order_relaxed); }
+ace_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return ACE_OK;
+  g_last_cuda_error = e;
+  return ACE_ERR_CUDA;
+}
 }  // namespace ace
 
 namespace ace {

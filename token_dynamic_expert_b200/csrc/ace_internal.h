@@ -24,6 +24,16 @@ constexpr int kDecodeMaxT = 8;    // token counts served by the decode kernel
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+// Byte range of `rows` rows of n elements of es bytes, ld elements apart;
+// empty for a null pointer.
+struct ByteSpan {
+  uintptr_t lo, hi;
+  ByteSpan(const void* p, int64_t ld, int64_t rows, int64_t n, size_t es)
+      : lo(reinterpret_cast<uintptr_t>(p)),
+        hi(p && rows > 0 ? lo + ((size_t)(rows - 1) * (size_t)ld + (size_t)n) * es : lo) {}
+  bool meets(const ByteSpan& o) const { return lo < o.hi && o.lo < hi; }
+};
+
 // Split of the router GEMM's K dimension for T tokens: enough CTAs to cover
 // the GPU twice, each split a multiple of the K step.
 int router_splitk(int T, int d, int E, int num_sms);
@@ -50,6 +60,8 @@ ace_status validate_layer(const ace_layer* L, bool need_experts);
 // decode kernel's grid barriers and the fused expert kernel's wait for a
 // tile's h rows.  Read when a call enqueues its kernels.
 uint64_t peer_wait_ns();
+// ACE_OK, or ACE_ERR_CUDA with the error kept for ace_last_cuda_error.
+ace_status cuda_status(cudaError_t e);
 // Zeroes n_words 32-bit words on the stream (the status block of a call).
 cudaError_t launch_clear_words(void* p, int n_words, cudaStream_t s);
 ace_status check_fusion(const ace_layer& L, int fusion);
