@@ -3,9 +3,11 @@
 Tolerances: s is one fp32 addition and one rounding, compared bit for bit.  The
 sum of squares of a row takes at most 16 additions in a thread and 10 across
 the CTA (26 half steps, 13 for its root), the mean, eps, root and reciprocal 4,
-the two products 2, and max, division by 127 2 more: 21, taken as 24.  h: expf 2
-ulp (4 half steps), 1 + e, the quotient, the product: 7, taken as 8.  Each
-result then rounds once to its type.  q has to be equal."""
+the two products 2, and max, division by 127 2 more: 21, taken as 24.  h: the
+base-2 exponential 2 ulp (4 half steps) with a correcting factor and its product
+(2), 1 + e, the reciprocal 1 ulp (2), two products (2): 11.  Each result then
+rounds once to its type, and the scale of h takes two products more (13).  q
+has to be equal."""
 import numpy as np
 import pytest
 import torch
@@ -142,10 +144,10 @@ def _swiglu(gu, want=("y", "q"), n_valid=None):
 def _check_swiglu(o, gu, dt):
     h, q, scale = ora.swiglu(ora.f64(gu))
     if "y" in o:
-        assert ora.close(ora.f64(o["y"]), h, ora.HALF[dt] + 8 * ora.U32, 1e-37) <= 1
+        assert ora.close(ora.f64(o["y"]), h, ora.HALF[dt] + 11 * ora.U32, 1e-37) <= 1
     if "q" in o:
         assert np.array_equal(o["q"].cpu().numpy(), q)
-        assert ora.close(ora.f64(o["q_scale"]), scale, 10 * ora.U32) <= 1
+        assert ora.close(ora.f64(o["q_scale"]), scale, 13 * ora.U32) <= 1
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])

@@ -5,7 +5,6 @@ current CUDA stream; every step of the computation runs in libace's kernels.
 There is no fallback: if ``libace.so`` is missing or fails to load, importing
 this module raises.
 """
-import contextlib
 import ctypes
 import os
 
@@ -293,51 +292,60 @@ def ace_moe_combine(slot_of, yslot, y, ws, stream=None):
     return y
 
 
-def _arg(t, name, dtype, shape):
-    """The pointer of an optional tensor argument, after its checks: dtype,
-    shape and C-contiguity."""
+# The 8-bit layer's operators are called once per step of a decode loop, where
+# the host's time a call counts: their checks read each property of a tensor
+# once and pass plain addresses.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda dev: torch.cuda.current_stream(dev).cuda_stream
+
+
+def _refuse(t, name, dev, dtype, shape):
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, is %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("tensors are on several devices: %s is not on device %d" % (name, dev))
+
+
+def _arg(t, name, dev, dtype, shape):
+    """The address of an optional tensor argument, after its checks: dtype,
+    shape, device and C-contiguity."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, is %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dev, dtype, shape)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return _ptr(t)
+    return t.data_ptr()
 
 
-def _rows(t, name, dtype, shape):
-    """(pointer, row stride) of an optional [rows][n] tensor whose rows may lie
+def _rows(t, name, dev, dtype, shape):
+    """(address, row stride) of an optional [rows][n] tensor whose rows may lie
     apart; elements of a row are neighbours."""
     if t is None:
         return None, 0
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, is %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
-    n = t.shape[1]
-    if (n > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < n):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dev, dtype, shape)
+    rows, n = shape
+    ld, step = t.stride()
+    if (n > 1 and step != 1) or (rows > 1 and ld < n):
         raise ValueError("%s must have rows of neighbouring elements" % name)
-    return _ptr(t), (t.stride(0) if t.shape[0] > 1 else n)
+    return t.data_ptr(), (ld if rows > 1 else n)
 
 
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on_device(*tensors):
-    """A context with the tensors' device as the current one: the library
-    launches on the current device, and the default stream is that device's."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
-                raise ValueError("tensors must be on a CUDA device, are on %s" % t.device)
-            if dev is not None and d != dev:
-                raise ValueError("tensors are on several devices: %d and %d" % (dev, d))
-            dev = d
-    return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+def _run(fn, name, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device as the current one (the
+    library launches on the current device, and the default stream is that
+    device's)."""
+    if dev < 0:
+        raise ValueError("%s: tensors must be on a CUDA device" % name)
+    if dev == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code != ACE_OK:
+        raise AceError(code, name)
 
 
 def ace_add_rmsnorm(x, gamma, residual=None, sum=None, y=None, q=None, q_scale=None, eps=1e-6,
@@ -348,18 +356,17 @@ def ace_add_rmsnorm(x, gamma, residual=None, sum=None, y=None, q=None, q_scale=N
     strided."""
     if x.dim() != 2:
         raise ValueError("x must be [T][d]")
-    T, d = x.shape
-    dt = _dtype_code(x)
-    px, ldx = _rows(x, "x", x.dtype, (T, d))
-    pr, ldr = _rows(residual, "residual", x.dtype, (T, d))
-    ps, lds = _rows(sum, "sum", x.dtype, (T, d))
-    py, ldy = _rows(y, "y", x.dtype, (T, d))
-    pq, ldq = _rows(q, "q", torch.int8, (T, d))
-    pg, pqs = _arg(gamma, "gamma", torch.float32, (d,)), _arg(q_scale, "q_scale", torch.float32, (T,))
-    with _on_device(x, gamma, residual, sum, y, q, q_scale):
-        code = _lib.ace_add_rmsnorm(px, ldx, pr, ldr, T, d, dt, pg, float(eps), ps, lds,
-                                    py, ldy, pq, ldq, pqs, _stream(stream))
-    _check(code, "ace_add_rmsnorm")
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    T, d = shape
+    code = _dtype_code(x)
+    px, ldx = _rows(x, "x", dev, dt, shape)
+    pr, ldr = _rows(residual, "residual", dev, dt, shape)
+    ps, lds = _rows(sum, "sum", dev, dt, shape)
+    py, ldy = _rows(y, "y", dev, dt, shape)
+    pq, ldq = _rows(q, "q", dev, torch.int8, shape)
+    _run(_lib.ace_add_rmsnorm, "ace_add_rmsnorm", dev, stream, px, ldx, pr, ldr, T, d, code,
+         _arg(gamma, "gamma", dev, torch.float32, (d,)), eps, ps, lds, py, ldy, pq, ldq,
+         _arg(q_scale, "q_scale", dev, torch.float32, (T,)))
 
 
 def ace_gate_topk(logits, idx, weight, bias=None, score="softmax", n_groups=1, topk_groups=1,
@@ -371,18 +378,15 @@ def ace_gate_topk(logits, idx, weight, bias=None, score="softmax", n_groups=1, t
     if logits.dim() != 2 or idx.dim() != 2:
         raise ValueError("logits must be [T][E] and idx [T][k]")
     T, E = logits.shape
-    k = idx.shape[1]
-    pl, ld = _rows(logits, "logits", logits.dtype, (T, E))
-    opts = ace_gate_opts(score=SCORES[score], n_groups=int(n_groups), topk_groups=int(topk_groups),
-                         group_score=GROUP_SCORES[group_score], renorm_topk=int(bool(renorm)),
-                         scale=float(scale), tau=float(tau))
-    args = (pl, ld, _dtype_code(logits), T, E, k, _arg(bias, "bias", torch.float32, (E,)),
-            ctypes.byref(opts), _arg(idx, "idx", torch.int32, (T, k)),
-            _arg(weight, "weight", torch.float32, (T, k)), _arg(factor, "factor", torch.float32, (E,)),
-            _arg(keep, "keep", torch.uint8, (T, k)))
-    with _on_device(logits, idx, weight, bias, factor, keep):
-        code = _lib.ace_gate_topk(*args, _stream(stream))
-    _check(code, "ace_gate_topk")
+    k, dev = idx.shape[1], logits.get_device()
+    pl, ld = _rows(logits, "logits", dev, logits.dtype, (T, E))
+    opts = ace_gate_opts(SCORES[score], n_groups, topk_groups, GROUP_SCORES[group_score],
+                         1 if renorm else 0, scale, tau)
+    _run(_lib.ace_gate_topk, "ace_gate_topk", dev, stream, pl, ld, _dtype_code(logits), T, E, k,
+         _arg(bias, "bias", dev, torch.float32, (E,)), opts,
+         _arg(idx, "idx", dev, torch.int32, (T, k)),
+         _arg(weight, "weight", dev, torch.float32, (T, k)),
+         _arg(factor, "factor", dev, torch.float32, (E,)), _arg(keep, "keep", dev, torch.uint8, (T, k)))
     return idx, weight
 
 
@@ -393,16 +397,14 @@ def ace_moe_group(idx, E, offsets, slot_of, keep=None, gate=None, slot_token=Non
     include/ace.h)."""
     if idx.dim() != 2:
         raise ValueError("idx must be [T][k]")
-    T, k = idx.shape
-    E = int(E)
-    args = (_arg(idx, "idx", torch.int32, (T, k)), _arg(keep, "keep", torch.uint8, (T, k)),
-            _arg(gate, "gate", torch.float32, (T, k)), T, k, E,
-            _arg(offsets, "offsets", torch.int32, (E + 1,)), _arg(slot_of, "slot_of", torch.int32, (T, k)),
-            _arg(slot_token, "slot_token", torch.int32, (T * k,)),
-            _arg(slot_gate, "slot_gate", torch.float32, (T * k,)))
-    with _on_device(idx, offsets, slot_of, keep, gate, slot_token, slot_gate):
-        code = _lib.ace_moe_group(*args, _stream(stream))
-    _check(code, "ace_moe_group")
+    shape, dev = idx.shape, idx.get_device()
+    T, k = shape
+    _run(_lib.ace_moe_group, "ace_moe_group", dev, stream, _arg(idx, "idx", dev, torch.int32, shape),
+         _arg(keep, "keep", dev, torch.uint8, shape), _arg(gate, "gate", dev, torch.float32, shape), T, k,
+         E, _arg(offsets, "offsets", dev, torch.int32, (E + 1,)),
+         _arg(slot_of, "slot_of", dev, torch.int32, shape),
+         _arg(slot_token, "slot_token", dev, torch.int32, (T * k,)),
+         _arg(slot_gate, "slot_gate", dev, torch.float32, (T * k,)))
     return offsets, slot_of
 
 
@@ -413,23 +415,24 @@ def ace_matmul_i8(xq, x_scale, wq, w_scale, out, ws, offsets=None, row_of=None, 
     row_of [S] reads the slots' rows of xq (see include/ace.h)."""
     if xq.dim() != 2 or out.dim() != 2 or wq.dim() not in (2, 3):
         raise ValueError("xq must be [n][K], wq [N][K] or [E][N][K], out [S][N]")
-    if wq.dim() == 3 and wq.shape[0] != 1 and offsets is None:
+    wshape, dev = wq.shape, xq.get_device()
+    E = wshape[0] if len(wshape) == 3 else 1
+    if E != 1 and offsets is None:
         raise ValueError("wq of several experts needs offsets")
-    E = wq.shape[0] if wq.dim() == 3 else 1
-    N, K = wq.shape[-2:]
+    N, K = wshape[-2:]
     n, S = xq.shape[0], out.shape[0]
-    px, ldx = _rows(xq, "xq", torch.int8, (n, K))
-    po, ldo = _rows(out, "out", out.dtype, (S, N))
-    p = ace_i8_product(xq=px, ldx=ldx, n_rows=n, x_scale=_arg(x_scale, "x_scale", torch.float32, (n,)),
-                       wq=_arg(wq, "wq", torch.int8, wq.shape),
-                       w_scale=_arg(w_scale, "w_scale", torch.float32, wq.shape[:-1]), E=E, N=N, K=K,
-                       offsets=_arg(offsets, "offsets", torch.int32, (E + 1,)),
-                       row_of=_arg(row_of, "row_of", torch.int32, (S,)),
-                       slot_scale=_arg(slot_scale, "slot_scale", torch.float32, (S,)))
-    args = (ctypes.byref(p), S, po, ldo, _dtype_code(out), _ptr(ws), ws.numel())
-    with _on_device(xq, x_scale, wq, w_scale, out, ws, offsets, row_of, slot_scale):
-        code = _lib.ace_matmul_i8(*args, _stream(stream))
-    _check(code, "ace_matmul_i8")
+    px, ldx = _rows(xq, "xq", dev, torch.int8, (n, K))
+    po, ldo = _rows(out, "out", dev, out.dtype, (S, N))
+    if ws.get_device() != dev:
+        raise ValueError("tensors are on several devices: ws is not on device %d" % dev)
+    p = ace_i8_product(px, ldx, n, _arg(x_scale, "x_scale", dev, torch.float32, (n,)),
+                       _arg(wq, "wq", dev, torch.int8, wshape),
+                       _arg(w_scale, "w_scale", dev, torch.float32, wshape[:-1]), E, N, K,
+                       _arg(offsets, "offsets", dev, torch.int32, (E + 1,)),
+                       _arg(row_of, "row_of", dev, torch.int32, (S,)),
+                       _arg(slot_scale, "slot_scale", dev, torch.float32, (S,)))
+    _run(_lib.ace_matmul_i8, "ace_matmul_i8", dev, stream, p, S, po, ldo, _dtype_code(out),
+         ws.data_ptr(), ws.numel() * ws.element_size())
     return out
 
 
@@ -439,15 +442,14 @@ def ace_swiglu(gu, y=None, q=None, q_scale=None, n_valid=None, stream=None):
     device) are left alone (see include/ace.h)."""
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gu must be [S][2 m]")
-    S, m = gu.shape[0], gu.shape[1] // 2
-    pgu, ldgu = _rows(gu, "gu", gu.dtype, (S, 2 * m))
-    py, ldy = _rows(y, "y", gu.dtype, (S, m))
-    pq, ldq = _rows(q, "q", torch.int8, (S, m))
-    args = (pgu, ldgu, S, m, _dtype_code(gu), _arg(n_valid, "n_valid", torch.int32, (1,)), py, ldy, pq,
-            ldq, _arg(q_scale, "q_scale", torch.float32, (S,)))
-    with _on_device(gu, y, q, q_scale, n_valid):
-        code = _lib.ace_swiglu(*args, _stream(stream))
-    _check(code, "ace_swiglu")
+    shape, dt, dev = gu.shape, gu.dtype, gu.get_device()
+    S, m = shape[0], shape[1] // 2
+    pgu, ldgu = _rows(gu, "gu", dev, dt, shape)
+    py, ldy = _rows(y, "y", dev, dt, (S, m))
+    pq, ldq = _rows(q, "q", dev, torch.int8, (S, m))
+    _run(_lib.ace_swiglu, "ace_swiglu", dev, stream, pgu, ldgu, S, m, _dtype_code(gu),
+         _arg(n_valid, "n_valid", dev, torch.int32, (1,)), py, ldy, pq, ldq,
+         _arg(q_scale, "q_scale", dev, torch.float32, (S,)))
 
 
 def _host_f32(t):

@@ -18,6 +18,7 @@
 // fp64 from the stored inputs, with M in fp64 too, so q is the correctly
 // rounded quotient; about one row in eight (d = 2048) has such an element.
 #include <math.h>
+#include <string.h>
 
 #include "ace_common.cuh"
 #include "ace_internal.h"
@@ -33,11 +34,127 @@ struct alignas(sizeof(T) * V) Vec {
   T e[V];
 };
 
-// Bits of |p|: as unsigned integers they order like the values, NaN above
-// infinity, so one integer maximum finds the largest and keeps a NaN.
-__device__ __forceinline__ uint32_t abs_bits(float p) { return __float_as_uint(p) & 0x7fffffffu; }
+// Two fp32 values in a register pair.  Blackwell's f32x2 instructions work on
+// both at once; these kernels are bound by instruction issue before HBM, and
+// the pairs halve their arithmetic.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 two(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 two(float a) { return two(a, a); }
+__device__ __forceinline__ float first(F2 a) {
+  return __uint_as_float((uint32_t)a);
+}
+__device__ __forceinline__ float second(F2 a) {
+  return __uint_as_float((uint32_t)(a >> 32));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
-__device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
+// Elements of a vector as fp32, and back with one rounding: bf16 by one shift
+// or mask an element and one conversion a pair.
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V>& a, float (&f)[V]) {
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    uint32_t w[V / 2];
+    memcpy(w, &a, sizeof(w));
+#pragma unroll
+    for (int c = 0; c < V / 2; ++c) {
+      f[2 * c] = __uint_as_float(w[c] << 16);
+      f[2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < V; ++c) f[c] = to_f(a.e[c]);
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> pack(const float (&f)[V]) {
+  Vec<T, V> a;
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int c = 0; c < V / 2; ++c)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[c]) : "f"(f[2 * c + 1]), "f"(f[2 * c]));
+    memcpy(&a, w, sizeof(w));
+  } else {
+#pragma unroll
+    for (int c = 0; c < V; ++c) a.e[c] = from_f<T>(f[c]);
+  }
+  return a;
+}
+
+// The low bytes of V words.
+template <int V>
+__device__ __forceinline__ Vec<int8_t, V> low_bytes(const uint32_t (&w)[V]) {
+  Vec<int8_t, V> o;
+  if constexpr (V % 4 == 0) {
+    uint32_t b[V / 4];
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c)
+      b[c] = __byte_perm(__byte_perm(w[4 * c], w[4 * c + 1], 0x0040),
+                         __byte_perm(w[4 * c + 2], w[4 * c + 3], 0x0040), 0x5410);
+    memcpy(&o, b, sizeof(b));
+  } else {
+#pragma unroll
+    for (int c = 0; c < V; ++c) o.e[c] = (int8_t)(w[c] & 0xffu);
+  }
+  return o;
+}
+
+// silu(g) u of a pair.  e^-g = 2^y with y = -g log2 e: the product's rounding
+// and the constant's are formed exactly enough (r) and put back as a factor
+// 1 + r ln 2, since 2^(y + r) = 2^y (1 + r ln 2 + ...) and |r| < 2^-16.
+// Relative error in half steps: ex2.approx 4, the factor 1 and its product 1,
+// 1 + e 1, rcp.approx 2, the two products 2: 11.  Above g = 128 e^-g is far
+// below half a step of 1; below g = -126 ln 2 the reciprocal underflows and
+// the result is 0.
+__device__ __forceinline__ F2 silu_mul(F2 g, F2 u) {
+  const F2 n = two(fmaxf(-first(g), -128.f), fmaxf(-second(g), -128.f));
+  const F2 y = mul2(n, two(-1.442695041f));  // -y
+  F2 r = fma2(n, two(1.442695041f), y);
+  r = fma2(n, two(1.925963033e-8f), r);  // log2 e = 1.44269502162933... + 1.92596e-8
+  float e0, e1, s0, s1;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(-first(y)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(-second(y)));
+  const F2 d = fma2(two(e0, e1), fma2(r, two(0.693147181f), two(1.f)), two(1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(first(d)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(second(d)));
+  return mul2(mul2(g, two(s0, s1)), u);
+}
+
+// max(m, |a|, |b|) that keeps a NaN of any (m is not negative).
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+template <int V>
+__device__ __forceinline__ float max_abs(float m, const float (&p)[V]) {
+#pragma unroll
+  for (int c = 0; c < V; c += 2) m = max_abs(m, p[c], c + 1 < V ? p[c + 1] : 0.f);
+  return m;
+}
+
+// The same in fp64, with the same limit below; and the nearest integer of
+// 127 w / top.  Calls, not inlined: rare, and large in registers.
+__device__ __noinline__ double silu_mul64(float g, float u) {
+  return g < -87.336545f ? 0.0 : (double)g / (1.0 + exp(-(double)g)) * (double)u;
+}
+__device__ __noinline__ int quotient64(double w, double top) {
+  return __double2int_rn(w * 127.0 / top);
+}
 
 struct RowArgs {
   const void* a;    // x, or gate|up rows
@@ -53,201 +170,211 @@ struct RowArgs {
   float eps;
 };
 
-// Relative error of v = p * (127 / M) in units of 2^-24.
-//   norm:   p 1 rounding, M 1, 127 / M 1, the product 1; + 2 for forming the interval   -> 8
-//   swiglu: h: expf 2 ulp (4 half steps), 1 + e, the division, the product (3) = 7;
-//           M 7; quotient 1, product 1; interval 2                                    -> 20
+// Relative error of p (127 / M) in units of 2^-24, and so half the width of the
+// interval that has to hold no half.
+//   norm:   p 1 rounding, M 1, 127 / M 1, its widening by the interval 1        -> 6
+//   swiglu: h 11 (silu_mul; 1 + e is formed with the factor's product, 1 less);
+//           M 11; 127 / M 1, widening 1                                         -> 24
 template <bool SWIGLU>
 __device__ __forceinline__ constexpr float rel_bound() {
-  return (SWIGLU ? 20.f : 8.f) * 5.9604645e-8f;
+  return (SWIGLU ? 24.f : 6.f) * 5.9604645e-8f;
 }
 
+// 1.5 x 2^23: fmaf(p, inv, kMagic) rounds p inv to the nearest integer (ties to
+// even) in one step, and its low byte is that integer in two's complement.
+constexpr float kMagic = 12582912.f;
+
+// An element's p in fp64, from the stored inputs.
+template <typename T>
+__device__ __forceinline__ double exact_p(const T* a, const float* gamma, float s, int d, int i,
+                                          bool swiglu) {
+  return swiglu ? silu_mul64(to_f(a[i]), to_f(a[d + i])) : (double)s * (double)gamma[i];
+}
+
+// gamma's V elements of vector `at` (16-byte loads from 4 elements on).
+template <int V>
+__device__ __forceinline__ void load_gamma(const float* gamma, int at, float (&g)[V]) {
+  constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+  for (int h = 0; h < V / W; ++h) {
+    const Vec<float, W> q = reinterpret_cast<const Vec<float, W>*>(gamma)[at * (V / W) + h];
+#pragma unroll
+    for (int c = 0; c < W; ++c) g[h * W + c] = q.e[c];
+  }
+}
+
+// One CTA per row.
 template <typename T, int V, int ITEMS, bool SWIGLU>
-__global__ void __launch_bounds__(1024) k_rows_i8(const RowArgs A) {
+__global__ void __launch_bounds__(V * ITEMS > 16 ? 512 : 1024) k_rows_i8(const RowArgs A) {
+  constexpr float kRel = rel_bound<SWIGLU>();
   __shared__ float s_ss[32];
   __shared__ uint32_t s_mx[32];
   __shared__ unsigned long long s_top;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nt = blockDim.x, nw = nt >> 5;
   const int64_t row = blockIdx.x;
-  if (SWIGLU && A.n_valid != nullptr && row >= *A.n_valid) return;  // uniform over the CTA
+  if (SWIGLU && A.n_valid != nullptr && row >= *A.n_valid) return;  // uniform over the row
   const T* a = static_cast<const T*>(A.a) + row * A.lda;
-  const T* b = A.b ? static_cast<const T*>(A.b) + row * A.ldb : nullptr;
   const int d = A.d, nv = d / V;
+  const T* b = SWIGLU ? a + d : A.b ? static_cast<const T*>(A.b) + row * A.ldb : nullptr;
   if (tid == 0) s_top = 0ull;
 
-  float v[ITEMS][V];  // norm: s; swiglu: h
-  float p[ITEMS][V];  // norm: s gamma; swiglu: unused (h)
-  float ss = 0.f;
-  uint32_t mx = 0u;
+  // every load of the row is in flight before the first is used
+  Vec<T, V> va[ITEMS], vb[ITEMS] = {};
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int at = i * blockDim.x + tid;
-    if (at >= nv) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) v[i][c] = p[i][c] = 0.f;
-      continue;
+    const int at = i * nt + tid;
+    if (at < nv) {
+      va[i] = reinterpret_cast<const Vec<T, V>*>(a)[at];
+      if (SWIGLU || b != nullptr) vb[i] = reinterpret_cast<const Vec<T, V>*>(b)[at];
     }
-    const Vec<T, V> va = reinterpret_cast<const Vec<T, V>*>(a)[at];
-    if constexpr (SWIGLU) {
-      const Vec<T, V> vu = reinterpret_cast<const Vec<T, V>*>(a + d)[at];
+  }
+  float v[ITEMS][V];  // norm: s; swiglu: h
+  float ss = 0.f, mx = 0.f;
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float g = to_f(va.e[c]);
-        v[i][c] = __fdiv_rn(g, 1.f + expf(-g)) * to_f(vu.e[c]);
-        mx = max(mx, abs_bits(v[i][c]));
+  for (int i = 0; i < ITEMS; ++i) {
+    const int at = i * nt + tid;
+    if (at >= nv) continue;
+    float w[V];
+    unpack(va[i], v[i]);
+    unpack(vb[i], w);
+    if constexpr (SWIGLU) {
+#pragma unroll
+      for (int c = 0; c < V; c += 2) {
+        const bool pair = c + 1 < V;
+        const F2 h = silu_mul(two(v[i][c], pair ? v[i][c + 1] : 0.f), two(w[c], pair ? w[c + 1] : 0.f));
+        v[i][c] = first(h);
+        if (pair) v[i][c + 1] = second(h);
       }
+      mx = max_abs(mx, v[i]);
     } else {
       if (b != nullptr) {
-        const Vec<T, V> vb = reinterpret_cast<const Vec<T, V>*>(b)[at];
-        Vec<T, V> vs;
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-          vs.e[c] = from_f<T>(to_f(va.e[c]) + to_f(vb.e[c]));
-          v[i][c] = to_f(vs.e[c]);
-        }
-        if (A.sum) reinterpret_cast<Vec<T, V>*>(static_cast<T*>(A.sum) + row * A.lds)[at] = vs;
-      } else {
-#pragma unroll
-        for (int c = 0; c < V; ++c) v[i][c] = to_f(va.e[c]);
-        if (A.sum) reinterpret_cast<Vec<T, V>*>(static_cast<T*>(A.sum) + row * A.lds)[at] = va;
+        for (int c = 0; c < V; ++c) v[i][c] += w[c];
+        va[i] = pack<T, V>(v[i]);
+        unpack(va[i], v[i]);
       }
-      const Vec<float, V> g = reinterpret_cast<const Vec<float, V>*>(A.gamma)[at];
+      if (A.sum) reinterpret_cast<Vec<T, V>*>(static_cast<T*>(A.sum) + row * A.lds)[at] = va[i];
+      float g[V], p[V];
+      load_gamma<V>(A.gamma, at, g);
 #pragma unroll
       for (int c = 0; c < V; ++c) {
         ss = fmaf(v[i][c], v[i][c], ss);
-        p[i][c] = v[i][c] * g.e[c];
-        mx = max(mx, abs_bits(p[i][c]));
+        p[c] = v[i][c] * g[c];
       }
+      mx = max_abs(mx, p);
     }
   }
-  mx = __reduce_max_sync(0xffffffffu, mx);
+  // the bits of non-negative floats order like the values, NaN above infinity
+  uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx) & 0x7fffffffu);
   if (!SWIGLU) ss = warp_sum(ss);
   if (lane == 0) {
-    s_mx[warp] = mx;
+    s_mx[warp] = mb;
     if (!SWIGLU) s_ss[warp] = ss;
   }
   __syncthreads();
-  mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_mx[lane] : 0u);
-  float r = 1.f;
-  if (!SWIGLU) {
-    ss = warp_sum(lane < nw ? s_ss[lane] : 0.f);
-    r = 1.0f / sqrtf(ss / (float)d + A.eps);
-  }
-  const float M = __uint_as_float(mx);
+  mb = __reduce_max_sync(0xffffffffu, lane < nw ? s_mx[lane] : 0u);
+  if (!SWIGLU) ss = warp_sum(lane < nw ? s_ss[lane] : 0.f);
+  const float r = SWIGLU ? 1.f : 1.0f / sqrtf(ss / (float)d + A.eps);
+  const float M = __uint_as_float(mb);
+  const bool finite = isfinite(M) && (SWIGLU || isfinite(ss));
+  const bool usable = finite && M >= 1.17549435e-38f;  // else no element to scale by: q = 0
+  const bool tiny = M < kTinyMax;
+  const float inv = usable && !tiny ? __fdiv_rn(127.f, M) : 0.f;
+  const float inv_lo = inv * (1.f - kRel), inv_hi = inv * (1.f + kRel);
+  uint32_t differ = usable && tiny ? 1u : 0u;
 
-  if (A.y != nullptr) {
-    Vec<T, V>* y = reinterpret_cast<Vec<T, V>*>(static_cast<T*>(A.y) + row * A.ldy);
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int at = i * blockDim.x + tid;
-      if (at >= nv) continue;
-      Vec<T, V> o;
-      if constexpr (SWIGLU) {
+  for (int i = 0; i < ITEMS; ++i) {
+    const int at = i * nt + tid;
+    if (at >= nv) continue;
+    float g[V];
+    if (!SWIGLU) load_gamma<V>(A.gamma, at, g);
+    if (A.y != nullptr) {
+      float o[V];
 #pragma unroll
-        for (int c = 0; c < V; ++c) o.e[c] = from_f<T>(v[i][c]);
-      } else {
-        const Vec<float, V> g = reinterpret_cast<const Vec<float, V>*>(A.gamma)[at];
+      for (int c = 0; c < V; ++c) o[c] = SWIGLU ? v[i][c] : xhat(v[i][c], r, g[c]);
+      reinterpret_cast<Vec<T, V>*>(static_cast<T*>(A.y) + row * A.ldy)[at] = pack<T, V>(o);
+    }
+    if (A.q != nullptr) {
+      uint32_t o[V];
 #pragma unroll
-        for (int c = 0; c < V; ++c) o.e[c] = from_f<T>(xhat(v[i][c], r, g.e[c]));
-      }
-      y[at] = o;
+      for (int c = 0; c < V; ++c) o[c] = 0u;
+      if (usable)  // the same for the whole row
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float p = SWIGLU ? v[i][c] : v[i][c] * g[c];
+          o[c] = __float_as_uint(fmaf(p, inv_lo, kMagic));
+          differ |= o[c] ^ __float_as_uint(fmaf(p, inv_hi, kMagic));
+        }
+      reinterpret_cast<Vec<int8_t, V>*>(A.q + row * A.ldq)[at] = low_bytes<V>(o);
     }
   }
   if (A.q == nullptr) return;
-
-  Vec<int8_t, V>* q = reinterpret_cast<Vec<int8_t, V>*>(A.q + row * A.ldq);
-  const bool finite = isfinite(M) && (SWIGLU || isfinite(ss));
-  if (!finite || M < 1.17549435e-38f) {  // uniform: no element to scale by
-    Vec<int8_t, V> z;
-#pragma unroll
-    for (int c = 0; c < V; ++c) z.e[c] = 0;
-    for (int at = tid; at < nv; at += blockDim.x) q[at] = z;
-    if (tid == 0) A.q_scale[row] = finite ? 0.f : __uint_as_float(0x7fc00000u);
-    return;
-  }
-  constexpr float kRel = rel_bound<SWIGLU>();
-  const bool tiny = M < kTinyMax;
-  const float inv = tiny ? 0.f : __fdiv_rn(127.f, M);
-  bool near = tiny;
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int at = i * blockDim.x + tid;
-    if (at >= nv) continue;
-    Vec<int8_t, V> o;
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float t = (SWIGLU ? v[i][c] : p[i][c]) * inv;
-      const int lo = __float2int_rn(t * (1.f - kRel)), hi = __float2int_rn(t * (1.f + kRel));
-      near |= lo != hi;
-      o.e[c] = (int8_t)lo;
-    }
-    q[at] = o;
-  }
-  if (tid == 0) A.q_scale[row] = M * r / 127.f;
-  if (!__syncthreads_or(near)) return;
+  if (tid == 0)
+    A.q_scale[row] = usable ? M * (r * (1.f / 127.f)) : finite ? 0.f : __uint_as_float(0x7fc00000u);
+  if (!__syncthreads_or((int)differ)) return;
 
   // fp64: first M, from the elements that fp32 cannot tell from the largest
   const float cand = M * (1.f - 4.f * kRel);
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int at = i * blockDim.x + tid;
+    const int at = i * nt + tid;
     if (at >= nv) continue;
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      if (!(fabsf(SWIGLU ? v[i][c] : p[i][c]) >= cand)) continue;
-      double w;
-      if constexpr (SWIGLU)
-        w = silu64((double)to_f(a[at * V + c])) * (double)to_f(a[d + at * V + c]);
-      else
-        w = (double)v[i][c] * (double)A.gamma[at * V + c];
-      atomicMax(&s_top, (unsigned long long)__double_as_longlong(fabs(w)));
+      const float p = SWIGLU ? v[i][c] : v[i][c] * A.gamma[at * V + c];
+      if (fabsf(p) >= cand)
+        atomicMax(&s_top, (unsigned long long)__double_as_longlong(
+                              fabs(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU))));
     }
   }
   __syncthreads();
   const double top = __longlong_as_double((long long)s_top);
-  if (!near) return;
+  if (differ == 0u) return;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int at = i * blockDim.x + tid;
+    const int at = i * nt + tid;
     if (at >= nv) continue;
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      const float t = (SWIGLU ? v[i][c] : p[i][c]) * inv;
-      if (!tiny && __float2int_rn(t * (1.f - kRel)) == __float2int_rn(t * (1.f + kRel))) continue;
-      double w;
-      if constexpr (SWIGLU)
-        w = silu64((double)to_f(a[at * V + c])) * (double)to_f(a[d + at * V + c]);
-      else
-        w = (double)v[i][c] * (double)A.gamma[at * V + c];
-      A.q[row * A.ldq + at * V + c] = (int8_t)__double2int_rn(w * 127.0 / top);
+      const float p = SWIGLU ? v[i][c] : v[i][c] * A.gamma[at * V + c];
+      if (tiny || fmaf(p, inv_lo, kMagic) != fmaf(p, inv_hi, kMagic))
+        A.q[row * A.ldq + at * V + c] =
+            (int8_t)quotient64(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU), top);
     }
   }
 }
 
+template <typename T, int V, int ITEMS, bool SWIGLU>
+cudaError_t launch_items(const RowArgs& A, cudaStream_t s) {
+  const int threads = cdiv(cdiv(cdiv(A.d, V), ITEMS), 32) * 32;
+  k_rows_i8<T, V, ITEMS, SWIGLU><<<(unsigned)A.rows, threads, 0, s>>>(A);
+  return cudaGetLastError();
+}
+
+// Vectors per thread.  Few rows: one, the shortest chain (2.3 us against 2.6
+// with two, one row of 2048).  Many rows: two of 16 bytes, enough loads in
+// flight with little work per row besides them (8191 rows of 2048 bf16: 1, 2,
+// 4, 8 vectors 35, 28, 31, 39 us); eight narrower ones (4000 rows of 2050: 8
+// and 16 of them 25 and 34 us).  SwiGLU's bf16 rows are bound by arithmetic and
+// take one (65536 rows of 512: 1 and 2 vectors 41.8 and 45 us).  More where a
+// row needs more than 1024 threads.
 template <typename T, int V, bool SWIGLU>
 cudaError_t launch_v(const RowArgs& A, cudaStream_t s) {
   const int nv = cdiv(A.d, V);
-  // about 256 threads a row; rows beyond that size take more threads, then
-  // more vectors a thread
-  int items = 1;
-  while (cdiv(nv, items) > 1024) items *= 2;
-  const int threads = cdiv(cdiv(nv, items), 32) * 32;
-  const dim3 grid((unsigned)A.rows);
-  if (items == 1)
-    k_rows_i8<T, V, 1, SWIGLU><<<grid, threads, 0, s>>>(A);
-  else if (items == 2)
-    k_rows_i8<T, V, 2, SWIGLU><<<grid, threads, 0, s>>>(A);
-  else if constexpr (V <= 4) {
-    if (items == 4) {
-      k_rows_i8<T, V, 4, SWIGLU><<<grid, threads, 0, s>>>(A);
-    } else if constexpr (V <= 2) {
-      if (items == 8)
-        k_rows_i8<T, V, 8, SWIGLU><<<grid, threads, 0, s>>>(A);
-      else if constexpr (V == 1)
-        k_rows_i8<T, V, 16, SWIGLU><<<grid, threads, 0, s>>>(A);
-    }
+  const bool few = A.rows < 2 * device_sm_count();
+  if constexpr (V >= 4) {
+    const int items = few || (SWIGLU && V == 8) ? 1 : 2;
+    if (items == 1 && nv <= 1024) return launch_items<T, V, 1, SWIGLU>(A, s);
+    if (nv <= 2048) return launch_items<T, V, 2, SWIGLU>(A, s);
+    if constexpr (V == 4) return launch_items<T, V, 4, SWIGLU>(A, s);
+  } else {
+    if (few && nv <= 1024) return launch_items<T, V, 1, SWIGLU>(A, s);
+    if (nv <= 8192) return launch_items<T, V, 8, SWIGLU>(A, s);
+    if constexpr (V == 1) return launch_items<T, V, 16, SWIGLU>(A, s);
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;  // not reached: d <= kMaxRow
 }
 
 // Whether every row can be moved in vectors of v elements.
