@@ -8,18 +8,25 @@
 // The integer sum is exact (|sum| <= 2^14 K < 2^31); it is rounded to fp32
 // once, then scaled, then rounded to the output type.
 //
-// Weight rows sit on the MMA's M side (128), slots on N (16..256): experts get
-// tens of slots while their matrices have hundreds of rows, and decode has a
-// handful of slots against whole matrices.  A work item is (slot tile, block of
-// 128 weight rows); items of one expert run row block by row block with its
-// tiles side by side, so that tiles after the first find the weights in L2.
-// The items of each expert follow from the offsets alone: every CTA scans them
-// into shared memory as it starts, so no launch prepares a tile list.
+// Weight rows sit on the MMA's M side, slots on N (16..256): experts get tens
+// of slots while their matrices have hundreds of rows, and decode has a handful
+// of slots against whole matrices.  A work item is (slot tile, block of weight
+// rows); items of one expert run row block by row block with its tiles side by
+// side, so that tiles after the first find the weights in L2.  The items of each
+// expert follow from the offsets alone: every CTA scans them into shared memory
+// as it starts, so no launch prepares a tile list.
 //
-//   warp 0    TMA producer: 128 x 128-byte boxes of weights; slot rows as
-//             boxes, or four rows an instruction (tile::gather4) through row_of
-//   warp 1    TMEM and the MMAs (one thread): four of K = 32 a stage
-//   warps 2-9 epilogue: tcgen05.ld, scales, stores
+// PAIR: a cluster of two CTAs works on one item (tcgen05 cta_group::2, 256
+// weight rows): each holds 128 of the rows and half of the slots, so a slot row
+// that a CTA loads feeds twice the MMA work.  Both CTAs' loads of a stage
+// complete on the leader's barrier, its MMA thread issues for both and commits
+// to both.  No TMA multicast.
+//
+//   warp 0       TMA producer: 128 x 128-byte boxes of weights, and of slot rows
+//   warp 1       TMEM and the MMAs (one thread): four of K = 32 a stage
+//   warps 2-9    epilogue: tcgen05.ld, scales, stores
+//   warps 10-13  with row_of: four slot rows an instruction (tile::gather4); one
+//                thread at a time issues these, so four warps share the issue
 // Two TMEM accumulators alternate between items, so an epilogue overlaps the
 // next main loop.  All waits are bounded.
 #include <math.h>
@@ -40,7 +47,10 @@ constexpr int kMaxN = 256;         // slots per tile
 constexpr int kStagesMax = 12;
 constexpr int kStageRoom = 200 * 1024;
 constexpr int kEpiWarps = 8;
-constexpr int kThreadsI8 = 64 + 32 * kEpiWarps;
+constexpr int kGatherWarp = 2 + kEpiWarps;  // the first of four
+constexpr int kGatherWarps = 4;
+constexpr int kThreadsI8 = 32 * (kGatherWarp + kGatherWarps);
+constexpr uint32_t kLeaderMask = 0xFEFFFFFFu;  // a barrier's address in the leader CTA
 constexpr uint32_t kTmemI8 = 512;
 
 struct MatArgs {
@@ -52,7 +62,7 @@ struct MatArgs {
   void* out;
   int64_t ldo;
   uint32_t* status;
-  int S, E, N, K, n_rows, tile, box;
+  int S, E, N, K, n_rows, tile, box;  // tile, box: slots per tile, rows per TMA box
 };
 
 struct SmemI8 {
@@ -71,27 +81,81 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
          | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_i8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                        uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-// Four rows (y0..y3) of the matrix at inner coordinate x, 128 bytes each, to
-// four consecutive 128-byte rows of shared memory.
-__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* m, int x, int y0,
-                                            int y1, int y2, int y3, uint64_t* bar,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y0), "r"(y1), "r"(y2),
-      "r"(y3), "l"(policy)
-      : "memory");
+// Arrive on `bar` (of both CTAs of a pair) once every MMA issued so far by this
+// thread has completed.
+template <bool PAIR>
+__device__ __forceinline__ void commit_i8(uint64_t* bar) {
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+// Box at (x, y) of the matrix, to shared memory; of a pair, completing on the
+// leader's barrier.
+template <bool PAIR>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* m, int x, int y,
+                                         uint64_t* bar, uint64_t policy) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar) & kLeaderMask), "r"(x), "r"(y),
+        "l"(policy)
+        : "memory");
+  else
+    tma_load_2d(dst, m, x, y, bar, policy);
+}
+
+// Four rows of the matrix at inner coordinate x, 128 bytes each, to four
+// consecutive 128-byte rows of shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void load_rows4(void* dst, const CUtensorMap* m, int x,
+                                           const int (&y)[4], uint64_t* bar, uint64_t policy) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4"
+        ".mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar) & kLeaderMask), "r"(x), "r"(y[0]),
+        "r"(y[1]), "r"(y[2]), "r"(y[3]), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+        ".mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y[0]), "r"(y[1]),
+        "r"(y[2]), "r"(y[3]), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&r)[16]) {
@@ -104,15 +168,30 @@ __device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&r)[16]) {
       : "r"(taddr));
 }
 
-// Slots per tile of an expert of cnt slots: near-equal, multiples of 16.
+// Slots per tile of an expert of cnt slots: near-equal, multiples of the MMA's
+// step of N (16; 32 for a pair).
+template <bool PAIR>
 __device__ __forceinline__ int tile_rows(int cnt, int ntile) {
-  return ((cnt + ntile - 1) / ntile + 15) & ~15;
+  constexpr int q = PAIR ? 32 : 16;
+  return ((cnt + ntile - 1) / ntile + q - 1) / q * q;
 }
 
 struct Item {
-  int e, row0, n, blk;
+  int e, row0, n, blk;  // expert, first slot, slots, block of weight rows
+  // slots each CTA of a pair holds (n for a CTA on its own, up to a step of N)
+  template <bool PAIR>
+  __device__ __forceinline__ int half() const {
+    return PAIR ? (n + 31) / 32 * 16 : (n + 15) / 16 * 16;
+  }
+  // groups of four slots that CTA `rank` gathers
+  template <bool PAIR>
+  __device__ __forceinline__ int groups(int rank) const {
+    const int h = half<PAIR>(), left = n - rank * h;
+    return (max(0, min(left, h)) + 3) / 4;
+  }
 };
 
+template <bool PAIR>
 __device__ __forceinline__ Item item_at(const SmemI8& sm, const MatArgs& A, int nblk, int w) {
   int lo = 0, hi = A.E - 1;  // the expert whose items hold w
   while (lo < hi) {
@@ -124,11 +203,11 @@ __device__ __forceinline__ Item item_at(const SmemI8& sm, const MatArgs& A, int 
   }
   const int l = w - sm.cum[lo], ntile = max(1, (sm.cum[lo + 1] - sm.cum[lo]) / nblk);
   const int cnt = sm.first[lo + 1] - sm.first[lo];
-  const int each = tile_rows(cnt, ntile), q = l % ntile;
+  const int each = tile_rows<PAIR>(cnt, ntile), q = l % ntile;
   return {lo, sm.first[lo] + q * each, max(0, min(each, cnt - q * each)), l / ntile};
 }
 
-template <typename TO>
+template <typename TO, bool PAIR>
 __global__ void __launch_bounds__(kThreadsI8, 1)
     k_matmul_i8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const MatArgs A) {
@@ -138,8 +217,14 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
   volatile int* abort_flag = &sm.abort_flag;
-  const int nblk = (A.N + kM - 1) / kM, ksteps = (A.K + kStepK - 1) / kStepK;
-  const int stage_bytes = kWBytes + A.tile * kStepK;
+  constexpr int kRows = PAIR ? 2 * kM : kM;  // weight rows per item
+  uint32_t rank = 0;
+  if (PAIR) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const bool leader = rank == 0;
+  const int w0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;  // first item, then every nw-th
+  const int nw = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  const int nblk = (A.N + kRows - 1) / kRows, ksteps = (A.K + kStepK - 1) / kStepK;
+  const int stage_bytes = kWBytes + A.tile / (PAIR ? 2 : 1) * kStepK;
   const int NS = min(kStagesMax, kStageRoom / stage_bytes);
 
   if (tid == 0) {
@@ -149,7 +234,7 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sm.tfull[a], 1);
-      mbar_init(&sm.tempty[a], 32 * kEpiWarps);
+      mbar_init(&sm.tempty[a], (PAIR ? 2 : 1) * 32 * kEpiWarps);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -158,11 +243,22 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
     tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
-    tmem_alloc(&sm.tmem, kTmemI8);
-    tmem_relinquish();
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&sm.tmem)),
+                   "r"(kTmemI8)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(&sm.tmem, kTmemI8);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR)
+    cluster_barrier();  // both CTAs' barriers exist before either signals the other
+  else
+    __syncthreads();
   tc_fence_after();
   // the experts' slots and items, two experts a thread
   int total;
@@ -204,64 +300,78 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
     // ------------------------------------------------------------ producer
     const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
     int stage = 0;
-    uint32_t phase = 0, issued = 0, issued_par = 0;
-    for (int w = blockIdx.x; w < total && !*abort_flag; w += gridDim.x) {
-      const Item it = item_at(sm, A, nblk, w);
-      int rows[2][4];  // gather: rows of slots 4 (lane + 32 h) ..
-      const int ng = (it.n + 3) / 4, nbox = (it.n + A.box - 1) / A.box;
-      if (A.row_of) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = 4 * (lane + 32 * h) + j;
-            const int r = c < it.n ? A.row_of[it.row0 + c] : 0;
-            rows[h][j] = r >= 0 && r < A.n_rows ? r : 0;  // the scale makes such a slot 0
-          }
-      }
-      const uint32_t bytes =
-          kWBytes + (A.row_of ? ng * 4 * kStepK : nbox * A.box * kStepK);
+    uint32_t phase = 0;
+    for (int w = w0; w < total && !*abort_flag; w += nw) {
+      const Item it = item_at<PAIR>(sm, A, nblk, w);
+      const int half = it.half<PAIR>(), row = it.row0 + (int)rank * half;
+      const int nbox = (half + A.box - 1) / A.box;
+      // the bytes that complete on this CTA's barrier: of a pair, both CTAs' on
+      // the leader's
+      uint32_t bytes = (PAIR ? 2u : 1u) * kWBytes;
+      if (A.row_of == nullptr)
+        bytes += (PAIR ? 2u : 1u) * (uint32_t)(nbox * A.box * kStepK);
+      else
+        bytes += (uint32_t)(it.groups<PAIR>(0) + (PAIR ? it.groups<PAIR>(1) : 0)) * 4 * kStepK;
       for (int kb = 0; kb < ksteps; ++kb) {
         if (!mbar_wait(&sm.empty[stage], phase ^ 1u, A.status, abort_flag)) break;
         __syncwarp();
         uint8_t* sw = smem + stage * stage_bytes;
-        uint8_t* sx = sw + kWBytes;
         if (lane == 0) {
-          mbar_expect_tx(&sm.full[stage], bytes);
-          tma_load_2d(sw, &tmW, kb * kStepK, it.e * A.N + it.blk * kM, &sm.full[stage], pol_w);
+          if (leader) mbar_expect_tx(&sm.full[stage], bytes);
+          load_box<PAIR>(sw, &tmW, kb * kStepK, it.e * A.N + it.blk * kRows + (int)rank * kM,
+                         &sm.full[stage], pol_w);
         }
         __syncwarp();
-        if (A.row_of) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (lane + 32 * h < ng)
-              tma_gather4(sx + (lane + 32 * h) * 4 * kStepK, &tmX, kb * kStepK, rows[h][0],
-                          rows[h][1], rows[h][2], rows[h][3], &sm.full[stage], pol_x);
-        } else if (lane < nbox) {
-          tma_load_2d(sx + lane * A.box * kStepK, &tmX, kb * kStepK, it.row0 + lane * A.box,
-                      &sm.full[stage], pol_x);
-        }
-        issued |= 1u << stage;
-        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (A.row_of == nullptr && lane < nbox)
+          load_box<PAIR>(sw + kWBytes + lane * A.box * kStepK, &tmX, kb * kStepK,
+                         row + lane * A.box, &sm.full[stage], pol_x);
         if (++stage == NS) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-    __syncwarp();
-    if (*abort_flag)  // let every copy this warp started land
-      for (int s = 0; s < NS; ++s)
-        if ((issued >> s) & 1u) mbar_drain(&sm.full[s], (issued_par >> s) & 1u);
+  } else if (warp >= kGatherWarp) {
+    // ------------------------------------------------- slot rows through row_of
+    if (A.row_of != nullptr) {
+      const uint64_t pol_x = policy_evict_last();
+      constexpr int kPer = kMaxN / 4 / kGatherWarps / (PAIR ? 2 : 1);  // groups a warp
+      const int g = (warp - kGatherWarp) * kPer + lane;
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int w = w0; w < total && !*abort_flag; w += nw) {
+        const Item it = item_at<PAIR>(sm, A, nblk, w);
+        const bool mine = lane < kPer && g < it.groups<PAIR>((int)rank);
+        int rows[4] = {0, 0, 0, 0};
+        if (mine)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = (int)rank * it.half<PAIR>() + 4 * g + j;
+            const int r = c < it.n ? A.row_of[it.row0 + c] : 0;
+            rows[j] = r >= 0 && r < A.n_rows ? r : 0;  // the scale makes such a slot 0
+          }
+        for (int kb = 0; kb < ksteps; ++kb) {
+          if (!mbar_wait(&sm.empty[stage], phase ^ 1u, A.status, abort_flag)) break;
+          __syncwarp();
+          if (mine)
+            load_rows4<PAIR>(smem + stage * stage_bytes + kWBytes + g * 4 * kStepK, &tmX,
+                             kb * kStepK, rows, &sm.full[stage], pol_x);
+          if (++stage == NS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (leader && lane == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-        const Item it = item_at(sm, A, nblk, w);
-        const uint32_t idesc = idesc_i8(kM, (max(it.n, 1) + 15) & ~15);
+      for (int w = w0; w < total && ok; w += nw) {
+        const Item it = item_at<PAIR>(sm, A, nblk, w);
+        const uint32_t idesc = idesc_i8(kRows, it.half<PAIR>() * (PAIR ? 2 : 1));
         if (!mbar_wait(&sm.tempty[acc], acc_phase ^ 1u, A.status, abort_flag)) break;
         tc_fence_after();
         const uint32_t d0 = tmem + (uint32_t)acc * 256u;
@@ -274,31 +384,39 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
           const uint32_t a0 = smem_u32(smem + stage * stage_bytes), b0 = a0 + kWBytes;
 #pragma unroll
           for (int kk = 0; kk < kStepK / 32; ++kk)
-            mma_i8(d0, sw128_kmajor_desc(a0 + kk * 32), sw128_kmajor_desc(b0 + kk * 32), idesc,
+            mma_i8<PAIR>(d0, sw128_kmajor_desc(a0 + kk * 32), sw128_kmajor_desc(b0 + kk * 32), idesc,
                    (kb | kk) != 0);
-          mma_commit(&sm.empty[stage]);
+          commit_i8<PAIR>(&sm.empty[stage]);
           if (++stage == NS) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        mma_commit(&sm.tfull[acc]);
+        commit_i8<PAIR>(&sm.tfull[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      mma_commit(&sm.drain);  // every MMA issued has completed before TMEM is freed
+      // every MMA issued has completed before TMEM is freed
+      if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_u32(&sm.drain))
+            : "memory");
+      else
+        mma_commit(&sm.drain);
       mbar_drain(&sm.drain, 0);
     }
-  } else {
+  } else if (warp < kGatherWarp) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; 16-slot groups taken
     const int et = tid - 64;
     int acc = 0;
     uint32_t acc_phase = 0;
     TO* out = static_cast<TO*>(A.out);
-    for (int w = blockIdx.x; w < total; w += gridDim.x) {
-      const Item it = item_at(sm, A, nblk, w);
+    bool alive = true;  // a warp whose wait ran out still meets the others' barriers
+    for (int w = w0; w < total; w += nw) {
+      const Item it = item_at<PAIR>(sm, A, nblk, w);
       // the tile's token scales, one thread a slot (the buffer's last readers
       // passed the previous item's barrier)
       float sc = 0.f;
@@ -308,10 +426,11 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
         if (r >= 0 && r < A.n_rows) sc = A.x_scale[r] * (A.slot_scale ? A.slot_scale[s] : 1.f);
       }
       sm.scale[acc][et] = sc;
-      const int col = it.blk * kM + q * 32 + lane;
+      const int col = it.blk * kRows + (int)rank * kM + q * 32 + lane;
       const float wsc = col < A.N ? A.w_scale[(size_t)it.e * A.N + col] : 0.f;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (!mbar_wait(&sm.tfull[acc], acc_phase, A.status, abort_flag)) break;
+      alive = alive && mbar_wait(&sm.tfull[acc], acc_phase, A.status, abort_flag);
+      if (!alive) continue;
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * 256u;
       for (int c0 = half * 16; c0 < it.n; c0 += 32) {
@@ -327,16 +446,40 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&sm.tempty[acc]);
+      if (PAIR)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         smem_u32(&sm.tempty[acc]) & kLeaderMask)
+                     : "memory");
+      else
+        mbar_arrive(&sm.tempty[acc]);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
   }
-  tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {
+    // a wait ran out somewhere: copies this CTA started may still be landing,
+    // so give them time before shared memory is given up
+    if (tid == 0) {
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 100000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  tc_fence_before();
+  if (PAIR)
+    cluster_barrier();  // both CTAs are done with TMEM and with each other's barriers
+  else
+    __syncthreads();
+  tc_fence_after();
   if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemI8);
+    if (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(kTmemI8)
+                   : "memory");
+    else
+      tmem_dealloc(tmem, kTmemI8);
   }
 }
 
@@ -375,15 +518,25 @@ bool map_i8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename TO>
+template <typename TO, bool PAIR>
 cudaError_t launch_mat(const CUtensorMap& w, const CUtensorMap& x, const MatArgs& A, int grid,
                        cudaStream_t s) {
-  const int smem = 1024 + kStageRoom;
-  cudaError_t e = cudaFuncSetAttribute(k_matmul_i8<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreadsI8);
+  cfg.dynamicSmemBytes = 1024 + kStageRoom;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = PAIR ? 2 : 1;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaFuncSetAttribute(
+      k_matmul_i8<TO, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
   if (e != cudaSuccess) return e;
-  k_matmul_i8<TO><<<grid, kThreadsI8, smem, s>>>(w, x, A);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, k_matmul_i8<TO, PAIR>, w, x, A);
 }
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -439,21 +592,31 @@ ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int64_t ldo,
   A.N = p->N;
   A.K = p->K;
   A.n_rows = p->n_rows;
-  const int sms = device_sm_count(), nblk = cdiv(p->N, kM);
-  // the largest tile that still gives every SM an item
+  const int sms = device_sm_count();
+  // The largest tile that still gives every SM an item; a pair of CTAs where
+  // tiles are large.
   A.tile = kMaxN;
-  while (A.tile > 16 && (int64_t)cdiv(S, A.tile) * nblk < sms) A.tile /= 2;
-  A.box = A.tile < 64 ? A.tile : 64;
-  // items of even slots: cdiv(S, tile) + E tiles at most
-  const int64_t items = ((int64_t)cdiv(S, A.tile) + (p->offsets ? p->E : 0)) * nblk;
+  while (A.tile > 16 && (int64_t)cdiv(S, A.tile) * cdiv(p->N, kM) < sms) A.tile /= 2;
+  const bool pair = A.tile >= 64 && p->N > kM;
+  A.box = pair ? 32 : A.tile < 64 ? A.tile : 64;
+  // even slots give cdiv(S, tile) + E tiles at most
+  const int64_t items = ((int64_t)cdiv(S, A.tile) + (p->offsets ? p->E : 0)) *
+                        cdiv(p->N, pair ? 2 * kM : kM);
   if (items > 0x3fffffff) return ACE_ERR_UNSUPPORTED;
   CUtensorMap tw, tx;
   if (!map_i8(&tw, p->wq, (uint64_t)p->E * p->N, p->K, p->K, kM) ||
       !map_i8(&tx, p->xq, p->n_rows, p->K, p->ldx, p->row_of ? 1 : A.box))
     return cuda_status(cudaErrorInvalidValue);
-  const int grid = items < sms ? (int)items : sms;
-  return cuda_status(out_dtype == ACE_BF16 ? launch_mat<__nv_bfloat16>(tw, tx, A, grid, s)
-                                           : launch_mat<float>(tw, tx, A, grid, s));
+  const int ctas = pair ? 2 * (int)(items < sms / 2 ? items : sms / 2)
+                        : (int)(items < sms ? items : sms);
+  cudaError_t e;
+  if (out_dtype == ACE_BF16)
+    e = pair ? launch_mat<__nv_bfloat16, true>(tw, tx, A, ctas, s)
+             : launch_mat<__nv_bfloat16, false>(tw, tx, A, ctas, s);
+  else
+    e = pair ? launch_mat<float, true>(tw, tx, A, ctas, s)
+             : launch_mat<float, false>(tw, tx, A, ctas, s);
+  return cuda_status(e);
 }
 
 }  // extern "C"
