@@ -63,12 +63,13 @@ struct MatArgs {
   int64_t ldo;
   uint32_t* status;
   int S, E, N, K, n_rows, tile, box;  // tile, box: slots per tile, rows per TMA box
+  bool pairs;                         // outputs can be stored two channels at a time
 };
 
 struct SmemI8 {
   int first[kMaxE + 1];  // first slot of each expert, then the slots in use
   int cum[kMaxE + 1];    // items of the experts before each
-  float scale[2][kMaxN];
+  alignas(16) float scale[kEpiWarps][kMaxN / 2];  // each epilogue warp's slots
   uint64_t full[kStagesMax], empty[kStagesMax], tfull[2], tempty[2], drain;
   int s_warp[32];
   uint32_t tmem;
@@ -158,14 +159,55 @@ __device__ __forceinline__ void cluster_barrier() {
                    : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&r)[16]) {
+// 32 lanes x 32 bit, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld32i(uint32_t taddr, int (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+// Outputs of 32 slots (n of them in use) of one channel a lane: v holds the
+// integer sums, scale the slots' factors, o the first slot's element of this
+// lane's channel.
+//   pairs (bf16, even N and ldo): neighbouring lanes exchange halves, so that
+//   the even lane stores two channels of the even slot and the odd lane two of
+//   the odd slot, in 4 bytes: half the stores
+//   else one element a store
+template <typename TO, bool FULL>
+__device__ __forceinline__ void store_slots(const int (&v)[32], const float* scale, float wsc,
+                                            TO* o, int64_t ldo, int n, bool in, bool pairs) {
+  if (sizeof(TO) == 2 && pairs) {
+    const bool odd = threadIdx.x & 1;
+    uint32_t* p = reinterpret_cast<uint32_t*>(o + (odd ? ldo - 1 : 0));
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(scale + c);
+      const float f[4] = {(float)v[c] * (s.x * wsc), (float)v[c + 1] * (s.y * wsc),
+                          (float)v[c + 2] * (s.z * wsc), (float)v[c + 3] * (s.w * wsc)};
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) {
+        uint32_t mine;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(mine) : "f"(f[h + 1]), "f"(f[h]));
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+        const uint32_t two = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+        if (in && (FULL || c + h + (odd ? 1 : 0) < n)) *p = two;
+        p += ldo;  // two slots of ldo elements, in units of two elements
+      }
+    }
+  } else if (in) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      if (FULL || c < n) *o = from_f<TO>((float)v[c] * (scale[c] * wsc));
+      o += ldo;
+    }
+  }
 }
 
 // Slots per tile of an expert of cnt slots: near-equal, multiples of the MMA's
@@ -234,7 +276,7 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sm.tfull[a], 1);
-      mbar_init(&sm.tempty[a], (PAIR ? 2 : 1) * 32 * kEpiWarps);
+      mbar_init(&sm.tempty[a], (PAIR ? 2 : 1) * kEpiWarps);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -409,49 +451,53 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
     }
   } else if (warp < kGatherWarp) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; 16-slot groups taken
-    const int et = tid - 64;
+    const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 slots
     int acc = 0;
     uint32_t acc_phase = 0;
     TO* out = static_cast<TO*>(A.out);
-    bool alive = true;  // a warp whose wait ran out still meets the others' barriers
+    float* scale = sm.scale[warp - 2];
     for (int w = w0; w < total; w += nw) {
       const Item it = item_at<PAIR>(sm, A, nblk, w);
-      // the tile's token scales, one thread a slot (the buffer's last readers
-      // passed the previous item's barrier)
-      float sc = 0.f;
-      if (et < it.n) {
-        const int s = it.row0 + et;
-        const int r = A.row_of ? A.row_of[s] : s;
-        if (r >= 0 && r < A.n_rows) sc = A.x_scale[r] * (A.slot_scale ? A.slot_scale[s] : 1.f);
+      // the factors of the slots this warp will store, ahead of the wait
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kMaxN / 64; ++i) {
+        const int c = part * 32 + i * 64 + lane, s = it.row0 + c;
+        float f = 0.f;
+        if (c < it.n) {
+          const int r = A.row_of ? A.row_of[s] : s;
+          if (r >= 0 && r < A.n_rows) f = A.x_scale[r] * (A.slot_scale ? A.slot_scale[s] : 1.f);
+        }
+        scale[i * 32 + lane] = f;
       }
-      sm.scale[acc][et] = sc;
+      __syncwarp();
       const int col = it.blk * kRows + (int)rank * kM + q * 32 + lane;
       const float wsc = col < A.N ? A.w_scale[(size_t)it.e * A.N + col] : 0.f;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      alive = alive && mbar_wait(&sm.tfull[acc], acc_phase, A.status, abort_flag);
-      if (!alive) continue;
+      if (!mbar_wait(&sm.tfull[acc], acc_phase, A.status, abort_flag)) break;
       tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * 256u;
-      for (int c0 = half * 16; c0 < it.n; c0 += 32) {
-        int v[16];
-        tmem_ld16i(tbase + (uint32_t)c0, v);
+      for (int c0 = part * 32; c0 < it.n; c0 += 64) {
+        int v[32];
+        tmem_ld32i(tbase + (uint32_t)c0, v);
         tmem_ld_wait();
-        if (col < A.N) {
-          TO* o = out + (size_t)(it.row0 + c0) * A.ldo + col;
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (c0 + c < it.n)
-              o[(size_t)c * A.ldo] = from_f<TO>((float)v[c] * (sm.scale[acc][c0 + c] * wsc));
-        }
+        TO* o = out + (size_t)(it.row0 + c0) * A.ldo + col;
+        if (c0 + 32 <= it.n)
+          store_slots<TO, true>(v, scale + c0 / 64 * 32, wsc, o, A.ldo, 32, col < A.N, A.pairs);
+        else
+          store_slots<TO, false>(v, scale + c0 / 64 * 32, wsc, o, A.ldo, it.n - c0, col < A.N, A.pairs);
       }
       tc_fence_before();
-      if (PAIR)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                         smem_u32(&sm.tempty[acc]) & kLeaderMask)
-                     : "memory");
-      else
-        mbar_arrive(&sm.tempty[acc]);
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR)
+          // orders TMEM reads alone; a release at cluster scope would wait for the
+          // warp's output stores, a microsecond an item
+          asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                           smem_u32(&sm.tempty[acc]) & kLeaderMask)
+                       : "memory");
+        else
+          mbar_arrive(&sm.tempty[acc]);
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -592,6 +638,7 @@ ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int64_t ldo,
   A.N = p->N;
   A.K = p->K;
   A.n_rows = p->n_rows;
+  A.pairs = out_dtype == ACE_BF16 && p->N % 2 == 0 && ldo % 2 == 0 && is_aligned(out, 4);
   const int sms = device_sm_count();
   // The largest tile that still gives every SM an item; a pair of CTAs where
   // tiles are large.
