@@ -10,16 +10,20 @@
 //   w_i = scale s_i [ / sum of the chosen s ]
 //   keep_i = i is the token's largest weight, or !(w_i A_e < tau)
 //
-// One warp per token.  A group lies on 32 / (groups rounded up to a power of
-// two) neighbouring lanes, so its value needs only shuffles inside them; a lane
-// sorts its experts once (packed as key << 32 | ~expert, largest first) and the
-// k rounds look at the lanes' heads.  Bound by latency: a chain of shuffles and
-// warp reductions per token, 8.9 MB of logits and results at 8192 x 256.
+// One warp per token.  A lane holds neighbouring experts, and a group lies on
+// 32 / (groups rounded up to a power of two) neighbouring lanes, so its value
+// needs only shuffles inside them, and of two equal keys the lower lane's is the
+// lower expert.  A lane sorts its experts once (packed as key << 32 | ~expert,
+// largest first) and leaves the list in shared memory; each of the k rounds takes
+// the largest of the lanes' heads by redux.max and moves one lane on.  Bound by
+// instruction issue and the latency of the rounds: the data are 8.9 MB at 8192
+// tokens of 256 experts.
 //
 // The choice is the one of exact arithmetic on the given logits: without a bias
 // it compares logits; with one, or where two groups' sums decide, scores whose
 // fp32 difference is within the error bound below are compared again in fp64
-// (a token in some hundreds).
+// (a token in some hundreds).  The scores that only decide are therefore formed
+// with the hardware's base-2 exponential; weights are formed with expf.
 #include <math.h>
 
 #include "ace_common.cuh"
@@ -38,21 +42,19 @@ struct GateArgs {
   int32_t* idx;
   float* weight;
   uint8_t* keep;  // or NULL
-  int T, E, k, sigmoid, G, topk_groups, top2, renorm, vec;
+  int T, E, k, sigmoid, G, lanes, topk_groups, top2, renorm, vec;
   float scale, tau;
 };
 
-// Where a lane's experts are: e0 + j * step for j < n, below end.
+// A lane's experts: e0 .. e0 + n - 1, of group `group`.
 struct LaneMap {
-  int e0, step, n, end, group;
+  int e0, n, group;
 };
 
 __device__ __forceinline__ LaneMap lane_map(const GateArgs& A, int lane, int lg) {
-  if (A.G == 1) return {lane, 32, (A.E + 31) / 32, A.E, 0};
   const int per = A.E / A.G, g = lane / lg, n = (per + lg - 1) / lg;
-  if (g >= A.G) return {0, 1, 0, 0, g};
-  const int e0 = g * per + (lane % lg) * n;
-  return {e0, 1, n, min(e0 + n, (g + 1) * per), g};
+  const int at = (lane % lg) * n;
+  return {g * per + at, g < A.G ? max(0, min(n, per - at)) : 0, g};
 }
 
 template <typename TL>
@@ -60,11 +62,21 @@ __device__ __forceinline__ float logit_at(const TL* row, int e) {
   return to_f(row[e]);
 }
 
-// fkey with -0 equal to +0 and every NaN above +infinity.  On the bits: the
-// sign and payload of a computed NaN are not to be relied on.
+__device__ __forceinline__ float exp2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// fkey with -0 equal to +0 and every NaN above +infinity, whatever its sign.
 __device__ __forceinline__ uint32_t gate_key(float v) {
-  const uint32_t b = __float_as_uint(v), a = b & 0x7fffffffu;
-  return a > 0x7f800000u ? 0xffffffffu : a == 0u ? 0x80000000u : fkey(v);
+  const uint32_t b = __float_as_uint(__fadd_rn(v, 0.f));
+  return v == v ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0xffffffffu;
 }
 
 // Largest two of the values held by the lg neighbouring lanes of a group.
@@ -79,120 +91,187 @@ __device__ __forceinline__ void group_top2(F& a, F& b, int lg) {
   }
 }
 
+// fkey for doubles (neither NaN nor -0: the callers add +0 and keep NaN out).
+__device__ __forceinline__ unsigned long long dkey(double v) {
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
+  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+
+// Largest 64-bit value over the warp, by its halves.
+__device__ __forceinline__ unsigned long long max64(unsigned long long v) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+  const uint32_t lo =
+      __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((unsigned long long)hi << 32) | lo;
+}
+
 // The choice in fp64 (see the head of the file); lane i < k receives rank i.
-template <typename TL>
+template <typename TL, int NV>
 __device__ __noinline__ int choose64(const GateArgs& A, const TL* row, int lane, int lg) {
   const LaneMap L = lane_map(A, lane, lg);
-  double m = -INFINITY, z = 0.0;
-  if (!A.sigmoid) {
-    float mf = -INFINITY;
-    for (int j = 0, e = L.e0; j < L.n && e < L.end; ++j, e += L.step)
-      mf = fmaxf(mf, logit_at(row, e));
-    for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, o));
-    m = isinf(mf) && mf < 0.f ? 0.0 : (double)mf;
-    for (int j = 0, e = L.e0; j < L.n && e < L.end; ++j, e += L.step)
-      z += exp((double)logit_at(row, e) - m);
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  double c[NV], m = 0.0, z = 1.0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) c[j] = j < L.n ? (double)logit_at(row, L.e0 + j) : -INFINITY;
+  const bool scored = A.bias != nullptr || A.top2;  // else experts compare by logit alone
+  if (scored) {
+    if (!A.sigmoid) {
+      float mf = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) mf = fmaxf(mf, (float)c[j]);
+      for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, o));
+      m = mf == -INFINITY ? 0.0 : (double)mf;
+      z = 0.0;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      c[j] = exp(A.sigmoid ? -c[j] : c[j] - m);
+      if (A.sigmoid)
+        c[j] = 1.0 / (1.0 + c[j]);
+      else if (j < L.n)
+        z += c[j];
+    }
+    if (!A.sigmoid)
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!A.sigmoid) c[j] = z > 0.0 ? c[j] / z : 0.0;
+      if (A.bias && j < L.n) c[j] += (double)A.bias[L.e0 + j];
+    }
   }
-  auto score = [&](int e) {
-    const double x = (double)logit_at(row, e);
-    if (A.sigmoid) return 1.0 / (1.0 + exp(-x));
-    return z > 0.0 ? exp(x - m) / z : 0.0;
-  };
   bool allowed = true;
   if (A.G > 1) {
     double a = -INFINITY, b = -INFINITY;
-    for (int j = 0, e = L.e0; j < L.n && e < L.end; ++j, e += L.step) {
-      const double c = A.bias ? score(e) + (double)A.bias[e]
-                              : (A.top2 ? score(e) : (double)logit_at(row, e));
-      if (c > a) {
-        b = a;
-        a = c;
-      } else if (c > b) {
-        b = c;
-      }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const double v = j < L.n ? c[j] : -INFINITY;
+      b = v > a ? a : (v > b ? v : b);
+      a = v > a ? v : a;
     }
     group_top2(a, b, lg);
-    const double gv = A.top2 && A.E / A.G > 1 ? a + b : a;
+    const unsigned long long gv = dkey(A.top2 && A.E / A.G > 1 ? a + b : a);
     int rank = 0;
     for (int h = 0; h < A.G; ++h) {
-      const double o = __shfl_sync(0xffffffffu, gv, h * lg);
+      const unsigned long long o = __shfl_sync(0xffffffffu, gv, h * lg);
       rank += o > gv || (o == gv && h < L.group);
     }
     allowed = L.group < A.G && rank < A.topk_groups;
   }
-  uint32_t taken = 0u;
+  uint32_t left = allowed ? (L.n >= 32 ? 0xffffffffu : (1u << L.n) - 1u) : 0u;
   int mine = 0;
   for (int i = 0; i < A.k; ++i) {
-    double best = -INFINITY;
-    int be = 0x7fffffff;
-    if (allowed)
-      for (int j = 0, e = L.e0; j < L.n && e < L.end; ++j, e += L.step) {
-        if ((taken >> j) & 1u) continue;
-        const double c = A.bias ? score(e) + (double)A.bias[e] : (double)logit_at(row, e);
-        if (be == 0x7fffffff || c > best) {
-          best = c;
-          be = e;
-        }
-      }
-    for (int o = 16; o > 0; o >>= 1) {
-      const double ob = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (oe != 0x7fffffff && (be == 0x7fffffff || ob > best || (ob == best && oe < be))) {
-        best = ob;
-        be = oe;
+    unsigned long long best = 0ull;
+    int bj = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      // without a bias experts compare by logit
+      const unsigned long long v =
+          (left >> j) & 1u ? dkey(A.bias ? c[j] : (double)logit_at(row, L.e0 + j)) : 0ull;
+      if (v > best) {
+        best = v;
+        bj = j;
       }
     }
-    for (int j = 0, e = L.e0; j < L.n && e < L.end; ++j, e += L.step)
-      if (e == be) taken |= 1u << j;
-    if (lane == i) mine = be;
+    const unsigned long long top = max64(best);  // every lane takes part
+    const uint32_t win = __ballot_sync(0xffffffffu, best != 0ull && best == top);
+    const int from = win ? __ffs((int)win) - 1 : 0;
+    const int e = __shfl_sync(0xffffffffu, L.e0 + bj, from);
+    if (lane == from) left &= ~(1u << bj);
+    if (lane == i) mine = e;
   }
   return mine;
 }
 
+// Puts the first k + 1 experts (lane i has that of rank i, or -1) in the order of
+// their fp64 choice values; lane i < k receives rank i.
 template <typename TL, int NV>
+__device__ __noinline__ int order64(const GateArgs& A, const TL* row, const LaneMap L, int lane,
+                                    int e) {
+  double m = 0.0, z = 1.0;
+  if (!A.sigmoid) {
+    float x[NV], mf = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      x[j] = j < L.n ? logit_at(row, L.e0 + j) : -INFINITY;
+      mf = fmaxf(mf, x[j]);
+    }
+    for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, o));
+    m = mf == -INFINITY ? 0.0 : (double)mf;
+    z = 0.0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) z += exp((double)x[j] - m);
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  const bool on = lane <= A.k && e >= 0;
+  double c = -INFINITY;
+  if (on) {
+    const double x = (double)logit_at(row, e);
+    c = A.sigmoid ? 1.0 / (1.0 + exp(-x)) : z > 0.0 ? exp(x - m) / z : 0.0;
+    c += (double)A.bias[e];
+  }
+  int rank = 0;
+  for (int j = 0; j <= A.k; ++j) {
+    const double o = __shfl_sync(0xffffffffu, c, j);
+    const int oe = __shfl_sync(0xffffffffu, e, j);
+    rank += oe >= 0 && (o > c || (o == c && oe < e));
+  }
+  int mine = 0;
+  for (int j = 0; j <= A.k; ++j) {
+    const int r = __shfl_sync(0xffffffffu, on ? rank : -1, j);
+    const int oe = __shfl_sync(0xffffffffu, e, j);
+    if (r == lane) mine = oe;
+  }
+  return mine;
+}
+
+// SIG: sigmoid scores, else softmax; BIAS: a balance bias is given.
+template <typename TL, int NV, bool SIG, bool BIAS>
 __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A) {
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  __shared__ unsigned long long s_list[kGateWarps][NV][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= A.T) return;
   const TL* row = static_cast<const TL*>(A.logits) + (size_t)t * A.ld;
-  int gp = 1;
-  while (gp < A.G) gp <<= 1;
-  const int lg = 32 / gp;
+  const int lg = A.lanes;  // lanes of a group
   const LaneMap L = lane_map(A, lane, lg);
-  const bool biased = A.bias != nullptr;
 
-  float x[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
+  float x[NV], bv[NV];
   constexpr int VL = NV < 4 ? 1 : 4;
-  if (VL > 1 && A.vec && L.n == NV) {  // a lane's neighbouring experts, 4 a load
+  if (VL > 1 && A.vec) {  // every lane has NV experts or none: 4 a load
+    struct alignas(sizeof(TL) * VL) QL {
+      TL e[VL];
+    };
 #pragma unroll
     for (int j = 0; j < NV; j += VL) {
-      struct alignas(sizeof(TL) * VL) Q {
-        TL e[VL];
-      };
-      const Q v = *reinterpret_cast<const Q*>(row + L.e0 + j);
+      if (L.n != 0) {
+        const QL v = *reinterpret_cast<const QL*>(row + L.e0 + j);
 #pragma unroll
-      for (int c = 0; c < VL; ++c) x[j + c] = to_f(v.e[c]);
+        for (int c = 0; c < VL; ++c) x[j + c] = to_f(v.e[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < VL; ++c) x[j + c] = -INFINITY;
+      }
+#pragma unroll
+      for (int c = 0; c < VL; ++c) bv[j + c] = 0.f;
+      if (BIAS && L.n != 0) {
+        const float4 b4 = *reinterpret_cast<const float4*>(A.bias + L.e0 + j);
+        bv[j] = b4.x;
+        bv[j + 1 < NV ? j + 1 : j] = b4.y;
+        bv[j + 2 < NV ? j + 2 : j] = b4.z;
+        bv[j + 3 < NV ? j + 3 : j] = b4.w;
+      }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = L.e0 + j * L.step;
-      if (j < L.n && e < L.end) x[j] = to_f(row[e]);
+      x[j] = j < L.n ? to_f(row[L.e0 + j]) : -INFINITY;
+      bv[j] = BIAS && j < L.n ? A.bias[L.e0 + j] : 0.f;
     }
   }
-  float bv[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e = L.e0 + j * L.step;
-    bv[j] = biased && j < L.n && e < L.end ? A.bias[e] : 0.f;
-  }
 
-  // softmax: maximum and sum over all experts
+  // softmax: maximum, and the sum where scores are asked for
+  constexpr float kLog2e = 1.442695041f;
   float m = 0.f, z = 1.f;
-  if (!A.sigmoid) {
+  if (!SIG) {
     m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NV; ++j) m = fmaxf(m, x[j]);
@@ -200,24 +279,32 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (m == -INFINITY) m = 0.f;  // nothing left: every score is 0
     z = 0.f;
-    if (biased || A.top2 || !A.renorm) {
+    if (!A.renorm) {  // weights are scores
 #pragma unroll
-      for (int j = 0; j < NV; ++j) z += x[j] == -INFINITY ? 0.f : expf(x[j] - m);
+      for (int j = 0; j < NV; ++j) z += expf(x[j] - m);
+      z = warp_sum(z);
+    } else if (BIAS || A.top2) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) z += exp2_approx((x[j] - m) * kLog2e);
       z = warp_sum(z);
     }
   }
   const float inv_z = z > 0.f ? 1.f / z : 0.f;
+  // a score to decide by, and one to weigh by
+  auto about = [&](float v) {
+    return SIG ? rcp_approx(1.f + exp2_approx(-kLog2e * v))
+                     : exp2_approx((v - m) * kLog2e) * inv_z;
+  };
   auto score = [&](float v) {
-    return A.sigmoid ? 1.f / (1.f + expf(-v)) : (v == -INFINITY ? 0.f : expf(v - m) * inv_z);
+    return SIG ? 1.f / (1.f + expf(-v)) : expf(v - m) * inv_z;
   };
 
   // keys, sorted largest first within the lane
   uint64_t c[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e = L.e0 + j * L.step;
-    const float key = biased ? score(x[j]) + bv[j] : x[j];
-    c[j] = j < L.n && e < L.end ? ((uint64_t)gate_key(key) << 32) | (uint64_t)(~(uint32_t)e) : 0ull;
+    const float key = BIAS ? about(x[j]) + bv[j] : x[j];
+    c[j] = j < L.n ? ((uint64_t)gate_key(key) << 32) | (uint64_t)(~(uint32_t)(L.e0 + j)) : 0ull;
   }
 #pragma unroll
   for (int p = 1; p < NV; p <<= 1)
@@ -236,13 +323,16 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
           }
         }
 
-  // Half the difference two exact scores may have where fp32 sees them equal:
-  // sigmoid: expf 2 ulp, the sum, the quotient: 4 x 2^-24 of s <= 1; softmax:
-  // the exponent's rounding (at most 0.37 x 2^-24 of the largest score), expf,
-  // and a sum of E <= 512 terms: 44 x 2^-24 of the largest score 1 / z; both:
-  // the addition of the bias, 2^-24 of c.  Doubled for two scores, and again
-  // for room.
-  const float err = A.sigmoid ? 9.6e-7f : 1.1e-5f * inv_z;
+  // How far two exact scores may lie apart where fp32 sees them equal, each in
+  // half steps (2^-24) of the scores' scale:
+  //   sigmoid: e^-x by ex2.approx 4 and its argument's rounding |x|, which change
+  //   s by their s (1 - s) fold, 1 + 0.23; 1 + e and the reciprocal 3: under 5
+  //   softmax, scale 1 / z: the exponent's roundings 2 d 2^-d..., under 1, ex2 4,
+  //   two products 2; the sum's terms likewise and its at most 32 + 5 additions:
+  //   under 64
+  // and the addition of the bias, half a step of c.  Twice for two scores, and
+  // again as room.
+  const float err = SIG ? 9.6e-7f : 1.1e-5f * inv_z;
   bool near = false;
 
   if (A.G > 1) {
@@ -251,9 +341,9 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     if (NV > 1 && c[NV > 1 ? 1 : 0] != 0ull) b = fkey_inv((uint32_t)(c[NV > 1 ? 1 : 0] >> 32));
     float gv;
     if (A.top2 && A.E / A.G > 1) {
-      if (!biased) {  // the keys are logits
-        a = c[0] != 0ull ? score(a) : a;
-        b = (NV > 1 && c[NV > 1 ? 1 : 0] != 0ull) ? score(b) : -INFINITY;
+      if (!BIAS) {  // the keys are logits
+        a = c[0] != 0ull ? about(a) : a;
+        b = (NV > 1 && c[NV > 1 ? 1 : 0] != 0ull) ? about(b) : -INFINITY;
       }
       group_top2(a, b, lg);
       gv = a + b;
@@ -270,7 +360,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
       rank += o > gk || (o == gk && h < L.group);
     }
     const bool allowed = L.group < A.G && rank < A.topk_groups;
-    if (biased || A.top2) {
+    if (BIAS || A.top2) {
       // the last group inside against the first outside
       const uint32_t last = __reduce_min_sync(0xffffffffu, allowed ? gk : 0xffffffffu);
       const uint32_t next = __reduce_max_sync(0xffffffffu, !allowed && L.group < A.G ? gk : 0u);
@@ -278,33 +368,36 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
           __reduce_max_sync(0xffffffffu, L.group < A.G ? __float_as_uint(mag) : 0u));
       near = next != 0u && fkey_inv(last) - fkey_inv(next) <= 2.f * (err + 4.8e-7f * top);
     }
-    if (!allowed) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) c[j] = 0ull;
-    }
+    if (!allowed) c[0] = 0ull;
   }
 
-  // k rounds; with a bias one more, for the border between k and k + 1
-  int my_e = 0;
-  uint32_t my_k = 0u;
-  const int rounds = A.k + (biased ? 1 : 0);
-  for (int i = 0; i < rounds; ++i) {
-    const uint32_t hk = (uint32_t)(c[0] >> 32);
-    const uint32_t mk = __reduce_max_sync(0xffffffffu, hk);
-    const uint32_t ne = __reduce_max_sync(0xffffffffu, hk == mk ? (uint32_t)c[0] : 0u);
-    const bool pop = mk != 0u && hk == mk && (uint32_t)c[0] == ne;
+  // k rounds; with a bias two more, for the border behind k
 #pragma unroll
-    for (int j = 0; j + 1 < NV; ++j) c[j] = pop ? c[j + 1] : c[j];
-    if (pop) c[NV - 1] = 0ull;
+  for (int j = 1; j < NV; ++j) s_list[warp][j][lane] = c[j];
+  uint64_t head = c[0];
+  int at = head != 0ull ? 0 : NV, my_e = 0;
+  uint32_t my_k = 0u;
+  const int rounds = A.k + (BIAS ? 2 : 0);
+  for (int i = 0; i < rounds; ++i) {
+    const uint32_t hk = (uint32_t)(head >> 32);
+    const uint32_t mk = __reduce_max_sync(0xffffffffu, hk);
+    // equal keys: the lower lane has the lower experts
+    const int from = __ffs((int)__ballot_sync(0xffffffffu, hk == mk)) - 1;
+    const uint32_t ne = __shfl_sync(0xffffffffu, (uint32_t)head, from);
+    if (lane == from) {  // its next expert (only this lane's own column is read)
+      ++at;
+      head = at < NV ? s_list[warp][at < NV ? at : 0][lane] : 0ull;
+    }
     if (lane == i) {
       my_e = mk != 0u ? (int)~ne : -1;
       my_k = mk;
     }
   }
   float my_x = -INFINITY;
-  if (biased) {
+  bool close = false;  // experts in question, none beyond the first k + 1
+  if (BIAS) {
     float my_b = 0.f;
-    if (lane <= A.k && my_e >= 0) {
+    if (lane < rounds && my_e >= 0) {
       my_x = logit_at(row, my_e);
       my_b = A.bias[my_e];
     }
@@ -314,10 +407,18 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     const float nb = __shfl_down_sync(0xffffffffu, my_b, 1);
     const float nvv = fkey_inv(nk);
     const bool same = nx == my_x && nb == my_b;  // a true tie: the index decides
-    if (lane < A.k && nk != 0u && !same)
-      near |= v - nvv <= 2.f * (err + 1.2e-7f * fmaxf(fabsf(v), fabsf(nvv)));
+    if (lane <= A.k && nk != 0u && !same &&
+        v - nvv <= 2.f * (err + 1.2e-7f * fmaxf(fabsf(v), fabsf(nvv)))) {
+      close = lane < A.k;
+      near |= lane == A.k;  // the one behind the border is in question too
+    }
   }
-  if (__any_sync(0xffffffffu, near)) my_e = choose64(A, row, lane, lg);
+  const bool all64 = __any_sync(0xffffffffu, near);
+  close = BIAS && __any_sync(0xffffffffu, close);
+  if (all64)
+    my_e = choose64<TL, NV>(A, row, lane, lg);
+  else if (close)
+    my_e = order64<TL, NV>(A, row, L, lane, my_e);
 
   // weights
   const bool on = lane < A.k;
@@ -328,16 +429,18 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     float top = on ? my_x : -INFINITY;
     const bool nan = __any_sync(0xffffffffu, on && my_x != my_x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (top != -INFINITY && on) {
-      if (!A.sigmoid) {
+      if (!SIG) {
         w = expf(my_x - top);
       } else {  // s = e^x / (1 + e^x); below 0 in units of e^min(top, 0)
         w = my_x > 0.f ? 1.f / (1.f + expf(-my_x))
                        : expf(my_x - fminf(top, 0.f)) / (1.f + expf(my_x));
       }
     }
-    const float sum = warp_sum(w);
+    float sum = w;  // the k <= 16 chosen lie on the first 16 lanes
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     w = nan ? __uint_as_float(0x7fffffffu) : (sum > 0.f ? w / sum : (sum != sum ? sum : 0.f));
   } else if (on) {
     w = score(my_x);
@@ -352,34 +455,44 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     // the token's largest weight (ties: the earlier slot) is always kept
     const uint32_t wk = on ? gate_key(w) : 0u;
     const uint32_t lead = __reduce_max_sync(0xffffffffu, wk);
-    const int first = __ffs((int)__ballot_sync(0xffffffffu, on && wk == lead)) - 1;
+    const int lead_lane = __ffs((int)__ballot_sync(0xffffffffu, on && wk == lead)) - 1;
     if (on)
       A.keep[(size_t)t * A.k + lane] =
-          lane == first || !(w * (A.factor ? A.factor[my_e] : 1.f) < A.tau);
+          lane == lead_lane || !(w * (A.factor ? A.factor[my_e] : 1.f) < A.tau);
   }
 }
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+template <typename TL, int NV>
+void launch_nv(const GateArgs& A, dim3 grid, dim3 block, cudaStream_t s) {
+  if (A.sigmoid && A.bias)
+    k_gate_topk<TL, NV, true, true><<<grid, block, 0, s>>>(A);
+  else if (A.sigmoid)
+    k_gate_topk<TL, NV, true, false><<<grid, block, 0, s>>>(A);
+  else if (A.bias)
+    k_gate_topk<TL, NV, false, true><<<grid, block, 0, s>>>(A);
+  else
+    k_gate_topk<TL, NV, false, false><<<grid, block, 0, s>>>(A);
+}
+
 template <typename TL>
 cudaError_t launch_gate(const GateArgs& A, cudaStream_t s) {
-  int gp = 1;
-  while (gp < A.G) gp <<= 1;
-  const int n = A.G == 1 ? cdiv(A.E, 32) : cdiv(A.E / A.G, 32 / gp);
+  const int n = cdiv(A.E / A.G, A.lanes);
   const int warps = A.T < kGateWarps ? A.T : kGateWarps;
   const dim3 grid((unsigned)cdiv(A.T, warps)), block((unsigned)(32 * warps));
   if (n <= 1)
-    k_gate_topk<TL, 1><<<grid, block, 0, s>>>(A);
+    launch_nv<TL, 1>(A, grid, block, s);
   else if (n <= 2)
-    k_gate_topk<TL, 2><<<grid, block, 0, s>>>(A);
+    launch_nv<TL, 2>(A, grid, block, s);
   else if (n <= 4)
-    k_gate_topk<TL, 4><<<grid, block, 0, s>>>(A);
+    launch_nv<TL, 4>(A, grid, block, s);
   else if (n <= 8)
-    k_gate_topk<TL, 8><<<grid, block, 0, s>>>(A);
+    launch_nv<TL, 8>(A, grid, block, s);
   else if (n <= 16)
-    k_gate_topk<TL, 16><<<grid, block, 0, s>>>(A);
+    launch_nv<TL, 16>(A, grid, block, s);
   else
-    k_gate_topk<TL, 32><<<grid, block, 0, s>>>(A);
+    launch_nv<TL, 32>(A, grid, block, s);
   return cudaGetLastError();
 }
 
@@ -426,12 +539,14 @@ ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype, int T,
   A.topk_groups = tg;
   A.top2 = A.G > 1 && opts->group_score == ACE_GROUP_TOP2;
   A.renorm = opts->renorm_topk != 0;
-  // a lane's experts are neighbours and start at a multiple of 4 of them
   int gp = 1;
   while (gp < A.G) gp <<= 1;
-  const int per = E / A.G, lg = 32 / gp;
-  A.vec = A.G > 1 && per % lg == 0 && (per / lg) % 4 == 0 && ld % 4 == 0 &&
-          is_aligned(logits, 4 * es);
+  A.lanes = 32 / gp;
+  // 4 logits a load where every lane in use holds the same number of experts, the
+  // template's NV (a power of two), and every address allows it
+  const int per = E / A.G, n = cdiv(per, A.lanes);
+  A.vec = per % n == 0 && n >= 4 && (n & (n - 1)) == 0 && ld % 4 == 0 &&
+          is_aligned(logits, 4 * es) && (!bias || is_aligned(bias, 16));
   A.scale = opts->scale;
   A.tau = opts->tau;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
