@@ -448,7 +448,7 @@ ACE_API ace_status ace_tau_quantile(const float* score, int n_tok, int k, int64_
  * checkpoints stored in 8 bits, and for routers with sigmoid scores, a
  * balance bias or groups of experts.  Used one after the other they make the
  * layer (token_dynamic_expert_b200/layer_i8.py):
- *     ace_add_rmsnorm -> router logits -> ace_gate_topk -> ace_moe_group ->
+ *     ace_add_rmsnorm -> ace_moe_logits -> ace_gate_topk -> ace_moe_group ->
  *     ace_matmul_i8 (gate and up) -> ace_swiglu -> ace_matmul_i8 (down) ->
  *     ace_moe_combine
  * Every call is asynchronous, allocates nothing and can be captured.  Row
@@ -482,6 +482,22 @@ ACE_API ace_status ace_add_rmsnorm(const void* x, int64_t ldx, const void* resid
                                    int T, int d, ace_dtype dtype, const float* gamma, float eps,
                                    void* sum, int64_t lds, void* y, int64_t ldy, int8_t* q,
                                    int64_t ldq, float* q_scale, void* stream);
+
+/* ------------------------------------------------------------------------
+ * ace_logits_workspace_size -- bytes of workspace ace_moe_logits needs for
+ *   `layer` and up to max_tokens tokens; 0 for an invalid layer.
+ *
+ * ace_moe_logits -- the router's logits on their own, for gates that
+ *   ace_moe_forward does not form (ace_gate_topk):
+ *     logits[t][e] = RMSNorm(u_t) gamma . w_e (+ router_bias[e])
+ *   by ace_moe_forward's kernels, the same bits.  u (device) [T][d]
+ *   layer->dtype, 16-byte aligned; logits (device) [T][E] fp32.  Of the layer
+ *   only d, E, dtype, gamma, w_router and router_bias are read (m and k have
+ *   to pass the layer checks).  Device flags: ace_read_status on ws.
+ * ---------------------------------------------------------------------- */
+ACE_API size_t ace_logits_workspace_size(const ace_layer* layer, int max_tokens);
+ACE_API ace_status ace_moe_logits(const ace_layer* layer, const void* u, int T, float eps_rms,
+                                  float* logits, void* ws, size_t ws_bytes, void* stream);
 
 /* Scores of ace_gate_topk, and what a group of experts is judged by. */
 typedef enum { ACE_SCORE_SOFTMAX = 0, ACE_SCORE_SIGMOID = 1 } ace_score;

@@ -148,3 +148,19 @@ def test_binding_refuses_what_the_kernels_cannot_see(ace):
                           torch.ones(2, 5), torch.zeros(3, 5), torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError, match="2 m"):
         ace.ace_swiglu(torch.zeros(3, 7))
+
+
+def test_logits_refuses(ace):
+    def call(T=4, u=P, eps=1e-6, logits=Q, ws=0xA000000, ws_bytes=1 << 30, **kw):
+        a = dict(d=256, E=8, m=64, k=1, dtype=0, gamma=R, w_router=R)
+        a.update(kw)
+        return ace.lib().ace_moe_logits(ctypes.byref(ace.ace_layer(**a)), u, T, eps, logits, ws, ws_bytes, None)
+
+    for bad in (dict(u=None), dict(logits=None), dict(T=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(gamma=None),
+                dict(w_router=None), dict(u=P + 8), dict(logits=Q + 2), dict(E=0)):
+        assert call(**bad) == ace.ACE_ERR_INVALID_ARG, bad
+    assert call(d=100) == ace.ACE_ERR_UNSUPPORTED
+    assert call(ws=None) == ace.ACE_ERR_WORKSPACE
+    assert call(ws_bytes=1024) == ace.ACE_ERR_WORKSPACE
+    bad = ace.ace_layer(d=256, E=8, m=64, k=1, dtype=0)
+    assert ace.lib().ace_logits_workspace_size(ctypes.byref(bad), 4) == 0

@@ -5,4 +5,4 @@ Python binding :mod:`token_dynamic_expert_b200.ace`.
 Importing the binding loads ``libace.so`` and raises if it is not built; the
 package has no CPU or eager fallback.
 """
-__all__ = ["ace", "build"]
+__all__ = ["ace", "build", "ep", "layer_i8"]

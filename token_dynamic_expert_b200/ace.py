@@ -116,6 +116,11 @@ _lib.ace_tau_workspace_size.restype = ctypes.c_size_t
 _lib.ace_tau_quantile.argtypes = [_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, _vp, _vp,
                                   ctypes.c_size_t, _vp]
 _lib.ace_tau_quantile.restype = ctypes.c_int
+_lib.ace_logits_workspace_size.argtypes = [_P(ace_layer), ctypes.c_int]
+_lib.ace_logits_workspace_size.restype = ctypes.c_size_t
+_lib.ace_moe_logits.argtypes = [_P(ace_layer), _vp, ctypes.c_int, ctypes.c_float, _vp, _vp,
+                                ctypes.c_size_t, _vp]
+_lib.ace_moe_logits.restype = ctypes.c_int
 _i64 = ctypes.c_int64
 _lib.ace_add_rmsnorm.argtypes = [_vp, _i64, _vp, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                  _vp, ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
@@ -367,6 +372,37 @@ def ace_add_rmsnorm(x, gamma, residual=None, sum=None, y=None, q=None, q_scale=N
     _run(_lib.ace_add_rmsnorm, "ace_add_rmsnorm", dev, stream, px, ldx, pr, ldr, T, d, code,
          _arg(gamma, "gamma", dev, torch.float32, (d,)), eps, ps, lds, py, ldy, pq, ldq,
          _arg(q_scale, "q_scale", dev, torch.float32, (T,)))
+
+
+def make_router_layer(gamma, w_router, router_bias=None):
+    """An ``ace_layer`` holding only gamma and the router (for
+    ace_moe_logits): E, d from w_router [E][d]."""
+    for t in (gamma, w_router, router_bias):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    E, d = w_router.shape
+    return ace_layer(d=d, E=E, m=64, k=1, dtype=_dtype_code(w_router), gamma=_ptr(gamma),
+                     w_router=_ptr(w_router), router_bias=_ptr(router_bias))
+
+
+def ace_logits_workspace_size(layer, max_tokens):
+    return int(_lib.ace_logits_workspace_size(layer, int(max_tokens)))
+
+
+def ace_moe_logits(layer, u, logits, ws, eps_rms=1e-6, stream=None):
+    """logits [T][E] fp32 = RMSNorm(u) gamma . w_router (+ bias) (see
+    include/ace.h); u [T][d] in the layer's dtype."""
+    dev = u.get_device()
+    if u.dim() != 2 or u.shape[1] != layer.d or _dtype_code(u) != layer.dtype:
+        raise ValueError("u must be [T][%d] in the layer's dtype" % layer.d)
+    T = u.shape[0]
+    if ws.get_device() != dev:
+        raise ValueError("tensors are on several devices: ws is not on device %d" % dev)
+    _run(_lib.ace_moe_logits, "ace_moe_logits", dev, stream, layer,
+         _arg(u, "u", dev, u.dtype, u.shape), T, eps_rms,
+         _arg(logits, "logits", dev, torch.float32, (T, layer.E)), ws.data_ptr(),
+         ws.numel() * ws.element_size())
+    return logits
 
 
 def ace_gate_topk(logits, idx, weight, bias=None, score="softmax", n_groups=1, topk_groups=1,

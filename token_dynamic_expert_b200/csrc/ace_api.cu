@@ -498,6 +498,44 @@ ace_status ace_moe_route(const ace_layer* layer, const void* u, int T, const ace
   return ACE_OK;
 }
 
+size_t ace_logits_workspace_size(const ace_layer* layer, int max_tokens) {
+  if (check_layer(layer, false) != ACE_OK || max_tokens < 0) return 0;
+  return fwd_layout(*layer, max_tokens, device_sm_count()).idx;  // the arrays ahead of the slots'
+}
+
+ace_status ace_moe_logits(const ace_layer* layer, const void* u, int T, float eps_rms,
+                          float* logits, void* ws, size_t ws_bytes, void* stream) {
+  ace_fwd_opts o = {};
+  o.eps_rms = eps_rms;
+  const ace_status st = check_common(layer, u, T, &o, ws, false);
+  if (st != ACE_OK) return st;
+  if (!(eps_rms >= 0.f) || (T > 0 && (!logits || !aligned(logits, 4)))) return ACE_ERR_INVALID_ARG;
+  const ace_layer& L = *layer;
+  const int num_sms = device_sm_count();
+  const FwdLayout ly = fwd_layout(L, T, num_sms);
+  if (ws_bytes < ly.idx) return ACE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const StatusClear clr = status_clear(ly, ws, false);
+  if (T == 0) {
+    ACE_CK(launch_clear_words(clr.p, clr.n, s));
+    return ACE_OK;
+  }
+  const bool tc = L.dtype == ACE_BF16;
+  const int splitk = router_splits_for(L, T, num_sms);
+  ACE_CK(launch_rmsnorm(L.dtype, u, T, L.d, L.gamma, eps_rms, at<float>(ws, ly.inv_rms), nullptr,
+                        clr.p, clr.n, nullptr, 0, L.w_router, L.E,
+                        tc ? at<void>(ws, ly.rw3) : nullptr, s));
+  if (tc)
+    ACE_CK(launch_router_tc(u, at<float>(ws, ly.inv_rms), at<void>(ws, ly.rw3), T, L.d, L.E,
+                            splitk, at<float>(ws, ly.part), at<uint32_t>(ws, ly.status), num_sms,
+                            s));
+  else
+    ACE_CK(launch_router_logits(L.dtype, u, at<float>(ws, ly.inv_rms), L.gamma, L.w_router, T,
+                                L.d, L.E, splitk, at<float>(ws, ly.part), s));
+  ACE_CK(launch_sum_splits(at<float>(ws, ly.part), splitk, T, L.E, L.router_bias, logits, num_sms, s));
+  return ACE_OK;
+}
+
 size_t ace_tau_workspace_size(void) { return tau_workspace_size(); }
 
 ace_status ace_tau_quantile(const float* score, int n_tok, int k, int64_t n_skip, float* tau,

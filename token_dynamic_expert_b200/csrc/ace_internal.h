@@ -83,6 +83,9 @@ cudaError_t launch_router_tc(const void* u, const float* inv_rms, const void* w3
 cudaError_t launch_router_logits(ace_dtype dt, const void* u, const float* inv_rms,
                                  const float* gamma, const void* wr, int T, int d, int E,
                                  int splitk, float* part, cudaStream_t s);
+// logits [T][E] from the partial sums part [splitk][T][E] (+ bias [E] or NULL)
+cudaError_t launch_sum_splits(const float* part, int splitk, int T, int E, const float* bias,
+                              float* logits, int num_sms, cudaStream_t s);
 struct ScanOut;
 struct FuseTables;
 cudaError_t launch_topk_mask(const float* part, int splitk, int T, int E, int k,

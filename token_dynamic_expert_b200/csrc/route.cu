@@ -180,6 +180,28 @@ __global__ void __launch_bounds__(256) k_router_logits(const T* __restrict__ u,
   }
 }
 
+// logits[i] = the split-K partial sums of element i in split order (+ bias), as
+// the top-k kernel adds them.
+__global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ part, int splitk,
+                                                    size_t n, int E, const float* __restrict__ bias,
+                                                    float* __restrict__ logits) {
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (size_t)gridDim.x * blockDim.x) {
+    float v = 0.f;
+#pragma unroll 4
+    for (int sp = 0; sp < splitk; ++sp) v += part[(size_t)sp * n + i];
+    logits[i] = bias ? v + bias[i % E] : v;
+  }
+}
+
+cudaError_t launch_sum_splits(const float* part, int splitk, int T, int E, const float* bias,
+                              float* logits, int num_sms, cudaStream_t s) {
+  const size_t n = (size_t)T * E, need = (n + 255) / 256, room = (size_t)num_sms * 8;
+  k_sum_splits<<<(unsigned)(need < room ? need : room), 256, 0, s>>>(part, splitk, n, E, bias,
+                                                                    logits);
+  return cudaGetLastError();
+}
+
 int router_splitk(int T, int d, int E, int num_sms) {
   const int tiles = cdiv(T, kRouterBT) * cdiv(E, kRouterBE);
   int s = cdiv(2 * num_sms, tiles);

@@ -1,0 +1,118 @@
+"""The routed SwiGLU layer with experts stored in 8-bit integers.
+
+One call runs, on the current stream and without a host synchronisation:
+
+1. the residual addition and the RMSNorm's int8 rows with a scale each:
+   ``ace_add_rmsnorm``;
+2. the router's logits from the sums, at fp32 accuracy: ``ace_moe_logits``;
+3. experts, weights and the ACE skip mask: ``ace_gate_topk``;
+4. the kept slots in expert order: ``ace_moe_group``;
+5. gate and up projections of the kept slots, their rows read through the
+   slots' tokens: ``ace_matmul_i8``;
+6. SiLU(gate) * up, to int8 rows: ``ace_swiglu``;
+7. the down projection, scaled by the slots' weights: ``ace_matmul_i8``;
+8. the sum of each token's slots in rank order: ``ace_moe_combine``.
+
+The number of kept slots stays on the device: buffers have room for every slot,
+and the kernels stop at the last one in use.  The buffers are allocated once
+(``LayerI8(..., max_tokens)``), so a call can be captured in a CUDA graph.
+Arithmetic is the operators' (see include/ace.h): integer sums are exact, int8
+rows are correctly rounded, everything else is fp32 with one rounding per stored
+result.
+"""
+import torch
+
+from . import ace
+
+
+def quantise_rows(w):
+    """int8 rows of w [..., n] and their fp32 scales [...]: q = nearest
+    integer of 127 w / max |w| of its row, scale = max |w| / 127 (0 for a row of
+    zeros).  Used once per checkpoint, to store weights in 8 bits."""
+    top = w.double().abs().amax(-1, keepdim=True)
+    q = torch.where(top > 0, torch.round(w.double() * 127.0 / top), 0.0)
+    return q.to(torch.int8), (top[..., 0] / 127.0).float()
+
+
+class LayerI8:
+    """Weights and buffers of one layer.
+
+    gamma [d] fp32; w_router [E][d] in the activations' type (bf16 or fp32); wq_gu [E][2 m][d] int8 (the
+    gate rows, then the up rows) with scales s_gu [E][2 m]; wq_down [E][d][m]
+    int8 with scales s_down [E][d]; bias [E] fp32 or None; factor [E] fp32 or None
+    (the ACE table of the skip rule).  d is a multiple of 64, m of 16.  gate: the
+    remaining arguments of ``ace.ace_gate_topk`` (score, n_groups, topk_groups,
+    group_score, renorm, scale)."""
+
+    def __init__(self, gamma, w_router, wq_gu, s_gu, wq_down, s_down, k, max_tokens, bias=None,
+                 factor=None, eps=1e-6, gate=None):
+        E, m2, d = wq_gu.shape
+        m = m2 // 2
+        if m2 % 2 or tuple(wq_down.shape) != (E, d, m) or tuple(w_router.shape) != (E, d):
+            raise ValueError("wq_gu [E][2 m][d], wq_down [E][d][m] and w_router [E][d] do not match")
+        if d % 64 or m % 16:
+            raise ValueError("d must be a multiple of 64 and m of 16, are %d and %d" % (d, m))
+        if max_tokens < 1 or not 1 <= k <= E:
+            raise ValueError("max_tokens must be positive and 1 <= k <= E")
+        self.gamma, self.bias, self.factor, self.eps = gamma, bias, factor, float(eps)
+        self.wq_gu, self.s_gu, self.wq_down, self.s_down = wq_gu, s_gu, wq_down, s_down
+        self.w_router, dtype = w_router, w_router.dtype
+        self.router = ace.make_router_layer(gamma, w_router)
+        self.E, self.d, self.m, self.k, self.max_tokens, self.dtype = E, d, m, int(k), int(max_tokens), dtype
+        self.gate = dict(gate or {})
+        dev, T, S = gamma.device, int(max_tokens), int(max_tokens) * int(k)
+        i32, f32, i8 = (dict(dtype=t, device=dev) for t in (torch.int32, torch.float32, torch.int8))
+        self.xq, self.xs = torch.empty(T, d, **i8), torch.empty(T, **f32)
+        self.sum, self.logits = torch.empty(T, d, dtype=dtype, device=dev), torch.empty(T, E, **f32)
+        self.idx, self.weight = torch.empty(S, **i32), torch.empty(S, **f32)
+        self.keep = torch.empty(S, dtype=torch.uint8, device=dev)
+        self.offsets, self.slot_of = torch.empty(E + 1, **i32), torch.empty(S, **i32)
+        self.slot_token, self.slot_gate = torch.empty(S, **i32), torch.empty(S, **f32)
+        self.gu = torch.empty(S, 2 * m, dtype=dtype, device=dev)
+        self.hq, self.hs = torch.empty(S, m, **i8), torch.empty(S, **f32)
+        self.yslot = torch.empty(S, d, dtype=dtype, device=dev)
+        # a workspace a call, so that each keeps its status word
+        self.ws = [ace.alloc_workspace(ace.ace_logits_workspace_size(self.router, T), dev)] + \
+            [ace.alloc_workspace(256, dev) for _ in range(3)]
+        for w in self.ws:
+            w.zero_()  # status() before the first call
+
+    def forward(self, u, y, residual=None, sum=None, tau=0.0, stream=None):
+        """y [T][d] = the layer's output for u [T][d] (+ residual; sum, if given,
+        receives u + residual, and may be either of them).  Slots but a token's
+        largest are skipped where weight * factor < tau.  T <= max_tokens."""
+        T, k, E = u.shape[0], self.k, self.E
+        if T > self.max_tokens or u.shape[1] != self.d or u.dtype != self.dtype:
+            raise ValueError("u must be [T <= %d][%d] %s" % (self.max_tokens, self.d, self.dtype))
+        if y.shape != u.shape or y.dtype != u.dtype:
+            raise ValueError("y must have u's shape and dtype")
+        if T == 0:
+            return y
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(u, y, residual, sum, tau)
+        S = T * k
+        xq, xs, logits = self.xq[:T], self.xs[:T], self.logits[:T]
+        if residual is not None and sum is None:
+            sum = self.sum[:T]
+        idx, weight, keep = (t[:S].view(T, k) for t in (self.idx, self.weight, self.keep))
+        slot_of, slot_token, slot_gate = self.slot_of[:S].view(T, k), self.slot_token[:S], self.slot_gate[:S]
+        gu, hq, hs, yslot = self.gu[:S], self.hq[:S], self.hs[:S], self.yslot[:S]
+        ace.ace_add_rmsnorm(u, self.gamma, residual=residual, sum=sum, q=xq, q_scale=xs, eps=self.eps)
+        ace.ace_moe_logits(self.router, u if sum is None else sum, logits, self.ws[0], eps_rms=self.eps)
+        ace.ace_gate_topk(logits, idx, weight, bias=self.bias, factor=self.factor, tau=tau, keep=keep,
+                          **self.gate)
+        ace.ace_moe_group(idx, E, self.offsets, slot_of, keep=keep, gate=weight, slot_token=slot_token,
+                          slot_gate=slot_gate)
+        ace.ace_matmul_i8(xq, xs, self.wq_gu, self.s_gu, gu, self.ws[1], offsets=self.offsets, row_of=slot_token)
+        ace.ace_swiglu(gu, q=hq, q_scale=hs, n_valid=self.offsets[E:])
+        ace.ace_matmul_i8(hq, hs, self.wq_down, self.s_down, yslot, self.ws[2], offsets=self.offsets,
+                          slot_scale=slot_gate)
+        ace.ace_moe_combine(slot_of, yslot, y, self.ws[3])
+        return y
+
+    def status(self, stream=None):
+        """(code, flags) of the last call, the first of its steps that is not
+        ACE_OK (synchronises)."""
+        codes = [ace.ace_read_status(w, stream) for w in self.ws]
+        return next((c for c in codes if c[0] != ace.ACE_OK), codes[-1])
