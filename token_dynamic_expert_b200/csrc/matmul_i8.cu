@@ -25,8 +25,10 @@
 //   warp 0       TMA producer: 128 x 128-byte boxes of weights, and of slot rows
 //   warp 1       TMEM and the MMAs (one thread): four of K = 32 a stage
 //   warps 2-9    epilogue: tcgen05.ld, scales, stores
-//   warps 10-13  with row_of: four slot rows an instruction (tile::gather4); one
-//                thread at a time issues these, so four warps share the issue
+//   warps 10-17  with row_of: four slot rows an instruction (tile::gather4).  A
+//                warp issues these one thread at a time, about 75 cycles each, so
+//                several warps share them (65536 gathered rows, 256 x 1024 x 2048:
+//                1, 4, 8 warps 591, 180, 172 us)
 // Two TMEM accumulators alternate between items, so an epilogue overlaps the
 // next main loop.  All waits are bounded.
 #include <math.h>
@@ -47,9 +49,12 @@ constexpr int kMaxN = 256;         // slots per tile
 constexpr int kStagesMax = 12;
 constexpr int kStageRoom = 200 * 1024;
 constexpr int kEpiWarps = 8;
-constexpr int kGatherWarp = 2 + kEpiWarps;  // the first of four
-constexpr int kGatherWarps = 4;
-constexpr int kThreadsI8 = 32 * (kGatherWarp + kGatherWarps);
+constexpr int kGatherWarp = 2 + kEpiWarps;  // the first of them
+constexpr int kGatherWarps = 8;
+// the gather warps exist with row_of only
+__host__ __device__ constexpr int threads_i8(bool gather) {
+  return 32 * (kGatherWarp + (gather ? kGatherWarps : 0));
+}
 constexpr uint32_t kLeaderMask = 0xFEFFFFFFu;  // a barrier's address in the leader CTA
 constexpr uint32_t kTmemI8 = 512;
 
@@ -249,8 +254,9 @@ __device__ __forceinline__ Item item_at(const SmemI8& sm, const MatArgs& A, int 
   return {lo, sm.first[lo] + q * each, max(0, min(each, cnt - q * each)), l / ntile};
 }
 
-template <typename TO, bool PAIR>
-__global__ void __launch_bounds__(kThreadsI8, 1)
+// GATHER: the slots' rows come through row_of.
+template <typename TO, bool PAIR, bool GATHER>
+__global__ void __launch_bounds__(threads_i8(GATHER), 1)
     k_matmul_i8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const MatArgs A) {
   extern __shared__ uint8_t smem_raw[];
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
       // the bytes that complete on this CTA's barrier: of a pair, both CTAs' on
       // the leader's
       uint32_t bytes = (PAIR ? 2u : 1u) * kWBytes;
-      if (A.row_of == nullptr)
+      if (!GATHER)
         bytes += (PAIR ? 2u : 1u) * (uint32_t)(nbox * A.box * kStepK);
       else
         bytes += (uint32_t)(it.groups<PAIR>(0) + (PAIR ? it.groups<PAIR>(1) : 0)) * 4 * kStepK;
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
                          &sm.full[stage], pol_w);
         }
         __syncwarp();
-        if (A.row_of == nullptr && lane < nbox)
+        if (!GATHER && lane < nbox)
           load_box<PAIR>(sw + kWBytes + lane * A.box * kStepK, &tmX, kb * kStepK,
                          row + lane * A.box, &sm.full[stage], pol_x);
         if (++stage == NS) {
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
     }
   } else if (warp >= kGatherWarp) {
     // ------------------------------------------------- slot rows through row_of
-    if (A.row_of != nullptr) {
+    if constexpr (GATHER) {
       const uint64_t pol_x = policy_evict_last();
       constexpr int kPer = kMaxN / 4 / kGatherWarps / (PAIR ? 2 : 1);  // groups a warp
       const int g = (warp - kGatherWarp) * kPer + lane;
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kThreadsI8, 1)
         const int c = part * 32 + i * 64 + lane, s = it.row0 + c;
         float f = 0.f;
         if (c < it.n) {
-          const int r = A.row_of ? A.row_of[s] : s;
+          const int r = GATHER ? A.row_of[s] : s;
           if (r >= 0 && r < A.n_rows) f = A.x_scale[r] * (A.slot_scale ? A.slot_scale[s] : 1.f);
         }
         scale[i * 32 + lane] = f;
@@ -564,12 +570,12 @@ bool map_i8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename TO, bool PAIR>
-cudaError_t launch_mat(const CUtensorMap& w, const CUtensorMap& x, const MatArgs& A, int grid,
+template <typename TO, bool PAIR, bool GATHER>
+cudaError_t launch_form(const CUtensorMap& w, const CUtensorMap& x, const MatArgs& A, int grid,
                        cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreadsI8);
+  cfg.blockDim = dim3(threads_i8(GATHER));
   cfg.dynamicSmemBytes = 1024 + kStageRoom;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -580,9 +586,19 @@ cudaError_t launch_mat(const CUtensorMap& w, const CUtensorMap& x, const MatArgs
   cfg.attrs = at;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaFuncSetAttribute(
-      k_matmul_i8<TO, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+      k_matmul_i8<TO, PAIR, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, k_matmul_i8<TO, PAIR>, w, x, A);
+  return cudaLaunchKernelEx(&cfg, k_matmul_i8<TO, PAIR, GATHER>, w, x, A);
+}
+
+template <typename TO>
+cudaError_t launch_mat(const CUtensorMap& w, const CUtensorMap& x, const MatArgs& A, bool pair,
+                       int grid, cudaStream_t s) {
+  if (A.row_of)
+    return pair ? launch_form<TO, true, true>(w, x, A, grid, s)
+                : launch_form<TO, false, true>(w, x, A, grid, s);
+  return pair ? launch_form<TO, true, false>(w, x, A, grid, s)
+              : launch_form<TO, false, false>(w, x, A, grid, s);
 }
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -640,11 +656,31 @@ ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int64_t ldo,
   A.n_rows = p->n_rows;
   A.pairs = out_dtype == ACE_BF16 && p->N % 2 == 0 && ldo % 2 == 0 && is_aligned(out, 4);
   const int sms = device_sm_count();
-  // The largest tile that still gives every SM an item; a pair of CTAs where
-  // tiles are large.
-  A.tile = kMaxN;
-  while (A.tile > 16 && (int64_t)cdiv(S, A.tile) * cdiv(p->N, kM) < sms) A.tile /= 2;
-  const bool pair = A.tile >= 64 && p->N > kM;
+  // Slots per tile, and whether pairs of CTAs work on it.
+  //   grouped: the largest tile that still gives every SM an item if experts were
+  //   full; tiles follow the experts' sizes below it.  Pairs from 64 slots on.
+  //   dense: the least rounds x rows loaded per item (16 for what an item costs
+  //   besides), as loads bound the kernel: 1500 and 512 slots of 2048 x 2048 take
+  //   12.4 and 10.5 us, with the grouped rule 16.7 and 14.4.
+  bool pair = false;
+  if (p->offsets) {
+    A.tile = kMaxN;
+    while (A.tile > 16 && (int64_t)cdiv(S, A.tile) * cdiv(p->N, kM) < sms) A.tile /= 2;
+    pair = A.tile >= 64 && p->N > kM;
+  } else {
+    int64_t best = INT64_MAX;
+    for (int t = 16; t <= kMaxN; t *= 2)
+      for (int two = 0; two <= (t >= 64 && p->N > kM ? 1 : 0); ++two) {
+        const int units = two ? sms / 2 : sms;
+        const int64_t items = (int64_t)cdiv(S, t) * cdiv(p->N, two ? 2 * kM : kM);
+        const int64_t cost = (items + units - 1) / units * (kM + (two ? t / 2 : t) + 16);
+        if (cost < best) {
+          best = cost;
+          A.tile = t;
+          pair = two != 0;
+        }
+      }
+  }
   A.box = pair ? 32 : A.tile < 64 ? A.tile : 64;
   // even slots give cdiv(S, tile) + E tiles at most
   const int64_t items = ((int64_t)cdiv(S, A.tile) + (p->offsets ? p->E : 0)) *
@@ -656,14 +692,8 @@ ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int64_t ldo,
     return cuda_status(cudaErrorInvalidValue);
   const int ctas = pair ? 2 * (int)(items < sms / 2 ? items : sms / 2)
                         : (int)(items < sms ? items : sms);
-  cudaError_t e;
-  if (out_dtype == ACE_BF16)
-    e = pair ? launch_mat<__nv_bfloat16, true>(tw, tx, A, ctas, s)
-             : launch_mat<__nv_bfloat16, false>(tw, tx, A, ctas, s);
-  else
-    e = pair ? launch_mat<float, true>(tw, tx, A, ctas, s)
-             : launch_mat<float, false>(tw, tx, A, ctas, s);
-  return cuda_status(e);
+  return cuda_status(out_dtype == ACE_BF16 ? launch_mat<__nv_bfloat16>(tw, tx, A, pair, ctas, s)
+                                           : launch_mat<float>(tw, tx, A, pair, ctas, s));
 }
 
 }  // extern "C"
