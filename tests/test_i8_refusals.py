@@ -68,7 +68,9 @@ def _gate(ace, **kw):
                                  dict(k=65), dict(dt=3), dict(score=2), dict(group_score=2), dict(n_groups=0),
                                  dict(n_groups=5), dict(topk_groups=0), dict(topk_groups=5), dict(ld=63),
                                  dict(n_groups=16, topk_groups=1), dict(scale=0.0), dict(scale=float("inf")),
-                                 dict(scale=float("nan")), dict(x=P + 2), dict(bias=Q + 1), dict(idx=Q + 2)])
+                                 dict(scale=float("nan")), dict(x=P + 2), dict(bias=Q + 1), dict(idx=Q + 2),
+                                 dict(idx=P), dict(w=P + 64), dict(w=Q + 32), dict(bias=Q), dict(keep=R + 4),
+                                 dict(factor=R)])
 def test_gate_refuses(ace, bad):
     assert _gate(ace, **bad) == ace.ACE_ERR_INVALID_ARG
 
@@ -88,7 +90,8 @@ def _group(ace, **kw):
 
 
 @pytest.mark.parametrize("bad", [dict(idx=None), dict(off=None), dict(so=None), dict(T=-1), dict(k=0), dict(k=17),
-                                 dict(E=0), dict(sg=P + 0x10000), dict(idx=P + 1), dict(off=Q + 2), dict(so=R + 1)])
+                                 dict(E=0), dict(sg=P + 0x10000), dict(idx=P + 1), dict(off=Q + 2), dict(so=R + 1),
+                                 dict(so=P), dict(so=Q + 16), dict(st=R), dict(keep=Q), dict(gate=R, sg=P + 0x10000)])
 def test_group_refuses(ace, bad):
     assert _group(ace, **bad) == ace.ACE_ERR_INVALID_ARG
 
@@ -157,7 +160,8 @@ def test_logits_refuses(ace):
         return ace.lib().ace_moe_logits(ctypes.byref(ace.ace_layer(**a)), u, T, eps, logits, ws, ws_bytes, None)
 
     for bad in (dict(u=None), dict(logits=None), dict(T=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(gamma=None),
-                dict(w_router=None), dict(u=P + 8), dict(logits=Q + 2), dict(E=0)):
+                dict(w_router=None), dict(u=P + 8), dict(logits=Q + 2), dict(E=0), dict(logits=P),
+                dict(logits=0xA000000)):
         assert call(**bad) == ace.ACE_ERR_INVALID_ARG, bad
     assert call(d=100) == ace.ACE_ERR_UNSUPPORTED
     assert call(ws=None) == ace.ACE_ERR_WORKSPACE

@@ -510,6 +510,10 @@ ace_status ace_moe_logits(const ace_layer* layer, const void* u, int T, float ep
   const ace_status st = check_common(layer, u, T, &o, ws, false);
   if (st != ACE_OK) return st;
   if (!(eps_rms >= 0.f) || (T > 0 && (!logits || !aligned(logits, 4)))) return ACE_ERR_INVALID_ARG;
+  const ByteSpan out(logits, layer->E, T, layer->E, 4);
+  if (out.meets(ByteSpan(u, layer->d, T, layer->d, esize(layer->dtype))) ||
+      out.meets(ByteSpan(ws, 1, (int64_t)ws_bytes, 1, 1)))
+    return ACE_ERR_INVALID_ARG;
   const ace_layer& L = *layer;
   const int num_sms = device_sm_count();
   const FwdLayout ly = fwd_layout(L, T, num_sms);
@@ -579,7 +583,7 @@ uint64_t ace_set_peer_wait_limit_ns(uint64_t ns) {
   return g_peer_wait_ns.exchange(ns == 0 ? kWaitLimitNs : ns);
 }
 
-const char* ace_version(void) { return "0.2.0"; }
+const char* ace_version(void) { return "0.3.0"; }
 
 const char* ace_last_cuda_error(void) { return cudaGetErrorString(g_last_cuda_error); }
 

@@ -148,7 +148,7 @@ __device__ __noinline__ int choose64(const GateArgs& A, const TL* row, int lane,
       a = v > a ? v : a;
     }
     group_top2(a, b, lg);
-    const unsigned long long gv = dkey(A.top2 && A.E / A.G > 1 ? a + b : a);
+    const unsigned long long gv = dkey(A.top2 ? a + b : a);
     int rank = 0;
     for (int h = 0; h < A.G; ++h) {
       const unsigned long long o = __shfl_sync(0xffffffffu, gv, h * lg);
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     if (c[0] != 0ull) a = fkey_inv((uint32_t)(c[0] >> 32));
     if (NV > 1 && c[NV > 1 ? 1 : 0] != 0ull) b = fkey_inv((uint32_t)(c[NV > 1 ? 1 : 0] >> 32));
     float gv;
-    if (A.top2 && A.E / A.G > 1) {
+    if (A.top2) {
       if (!BIAS) {  // the keys are logits
         a = c[0] != 0ull ? about(a) : a;
         b = (NV > 1 && c[NV > 1 ? 1 : 0] != 0ull) ? about(b) : -INFINITY;
@@ -523,6 +523,16 @@ ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype, int T,
   if (!logits || !idx || !weight || !is_aligned(logits, es) || !is_aligned(idx, 4) ||
       !is_aligned(weight, 4) || !is_aligned(bias, 4) || !is_aligned(factor, 4) || ld < E)
     return ACE_ERR_INVALID_ARG;
+  const ByteSpan in[3] = {ByteSpan(logits, ld, T, E, es), ByteSpan(bias, 1, E, 1, 4),
+                          ByteSpan(factor, 1, E, 1, 4)};
+  const ByteSpan out[3] = {ByteSpan(idx, k, T, k, 4), ByteSpan(weight, k, T, k, 4),
+                           ByteSpan(keep, k, T, k, 1)};
+  for (int o = 0; o < 3; ++o) {
+    for (const ByteSpan& i : in)
+      if (out[o].meets(i)) return ACE_ERR_INVALID_ARG;
+    for (int p = 0; p < o; ++p)
+      if (out[o].meets(out[p])) return ACE_ERR_INVALID_ARG;
+  }
   GateArgs A;
   A.logits = logits;
   A.ld = ld;
@@ -537,7 +547,7 @@ ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype, int T,
   A.sigmoid = opts->score == ACE_SCORE_SIGMOID;
   A.G = tg == G ? 1 : G;  // every group allowed: no limit
   A.topk_groups = tg;
-  A.top2 = A.G > 1 && opts->group_score == ACE_GROUP_TOP2;
+  A.top2 = A.G > 1 && E > A.G && opts->group_score == ACE_GROUP_TOP2;  // of one expert: its own
   A.renorm = opts->renorm_topk != 0;
   int gp = 1;
   while (gp < A.G) gp <<= 1;

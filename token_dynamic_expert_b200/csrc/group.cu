@@ -217,6 +217,17 @@ ace_status ace_moe_group(const int32_t* idx, const uint8_t* keep, const float* g
   if (!is_aligned(idx, 4) || !is_aligned(gate, 4) || !is_aligned(offsets, 4) ||
       !is_aligned(slot_of, 4) || !is_aligned(slot_token, 4) || !is_aligned(slot_gate, 4))
     return ACE_ERR_INVALID_ARG;
+  const int64_t S = (int64_t)T * k;
+  const ByteSpan in[3] = {ByteSpan(idx, 1, S, 1, 4), ByteSpan(keep, 1, S, 1, 1),
+                          ByteSpan(gate, 1, S, 1, 4)};
+  const ByteSpan out[4] = {ByteSpan(offsets, 1, E + 1, 1, 4), ByteSpan(slot_of, 1, S, 1, 4),
+                           ByteSpan(slot_token, 1, S, 1, 4), ByteSpan(slot_gate, 1, S, 1, 4)};
+  for (int o = 0; o < 4; ++o) {
+    for (const ByteSpan& i : in)
+      if (out[o].meets(i)) return ACE_ERR_INVALID_ARG;
+    for (int p = 0; p < o; ++p)
+      if (out[o].meets(out[p])) return ACE_ERR_INVALID_ARG;
+  }
   const GroupArgs A = {idx, keep, gate, offsets, slot_of, slot_token, slot_gate, T * k, T, k, E};
   return cuda_status(launch_group(A, static_cast<cudaStream_t>(stream)));
 }

@@ -91,6 +91,9 @@ class LayerI8:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.forward(u, y, residual, sum, tau)
+        if u.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(u.device):
+                return self.forward(u, y, residual, sum, tau)
         S = T * k
         xq, xs, logits = self.xq[:T], self.xs[:T], self.logits[:T]
         if residual is not None and sum is None:
@@ -114,5 +117,6 @@ class LayerI8:
     def status(self, stream=None):
         """(code, flags) of the last call, the first of its steps that is not
         ACE_OK (synchronises)."""
-        codes = [ace.ace_read_status(w, stream) for w in self.ws]
+        with torch.cuda.device(self.ws[0].device):
+            codes = [ace.ace_read_status(w, stream) for w in self.ws]
         return next((c for c in codes if c[0] != ace.ACE_OK), codes[-1])
