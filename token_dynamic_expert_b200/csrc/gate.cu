@@ -28,6 +28,7 @@
 
 #include "ace_common.cuh"
 #include "ace_internal.h"
+#include "launch.cuh"
 
 namespace ace {
 namespace {
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
   __shared__ unsigned long long s_list[kGateWarps][NV][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
+  begin_overlapped();
   if (t >= A.T) return;
   const TL* row = static_cast<const TL*>(A.logits) + (size_t)t * A.ld;
   const int lg = A.lanes;  // lanes of a group
@@ -465,35 +467,25 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 template <typename TL, int NV>
-void launch_nv(const GateArgs& A, dim3 grid, dim3 block, cudaStream_t s) {
-  if (A.sigmoid && A.bias)
-    k_gate_topk<TL, NV, true, true><<<grid, block, 0, s>>>(A);
-  else if (A.sigmoid)
-    k_gate_topk<TL, NV, true, false><<<grid, block, 0, s>>>(A);
-  else if (A.bias)
-    k_gate_topk<TL, NV, false, true><<<grid, block, 0, s>>>(A);
-  else
-    k_gate_topk<TL, NV, false, false><<<grid, block, 0, s>>>(A);
+cudaError_t launch_nv(const GateArgs& A, cudaStream_t s) {
+  const int warps = A.T < kGateWarps ? A.T : kGateWarps;
+  const unsigned grid = (unsigned)cdiv(A.T, warps), block = 32u * warps;
+  if (A.sigmoid)
+    return A.bias ? launch_overlapped(k_gate_topk<TL, NV, true, true>, grid, block, 1, 0, s, A)
+                  : launch_overlapped(k_gate_topk<TL, NV, true, false>, grid, block, 1, 0, s, A);
+  return A.bias ? launch_overlapped(k_gate_topk<TL, NV, false, true>, grid, block, 1, 0, s, A)
+                : launch_overlapped(k_gate_topk<TL, NV, false, false>, grid, block, 1, 0, s, A);
 }
 
 template <typename TL>
 cudaError_t launch_gate(const GateArgs& A, cudaStream_t s) {
   const int n = cdiv(A.E / A.G, A.lanes);
-  const int warps = A.T < kGateWarps ? A.T : kGateWarps;
-  const dim3 grid((unsigned)cdiv(A.T, warps)), block((unsigned)(32 * warps));
-  if (n <= 1)
-    launch_nv<TL, 1>(A, grid, block, s);
-  else if (n <= 2)
-    launch_nv<TL, 2>(A, grid, block, s);
-  else if (n <= 4)
-    launch_nv<TL, 4>(A, grid, block, s);
-  else if (n <= 8)
-    launch_nv<TL, 8>(A, grid, block, s);
-  else if (n <= 16)
-    launch_nv<TL, 16>(A, grid, block, s);
-  else
-    launch_nv<TL, 32>(A, grid, block, s);
-  return cudaGetLastError();
+  if (n <= 1) return launch_nv<TL, 1>(A, s);
+  if (n <= 2) return launch_nv<TL, 2>(A, s);
+  if (n <= 4) return launch_nv<TL, 4>(A, s);
+  if (n <= 8) return launch_nv<TL, 8>(A, s);
+  if (n <= 16) return launch_nv<TL, 16>(A, s);
+  return launch_nv<TL, 32>(A, s);
 }
 
 }  // namespace

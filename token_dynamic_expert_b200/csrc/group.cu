@@ -21,6 +21,7 @@
 #include "ace_common.cuh"
 #include "ace_internal.h"
 #include "compact.cuh"
+#include "launch.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(kGroupThreads) k_group(const GroupArgs A) {
     bits[i] = 0u;
   }
   __syncwarp();
+  begin_overlapped();
   // The chunk's slots x = 32 j + lane: experts of kept slots, else -1.  Every load
   // is in flight before the first is used.
   int e[kMaxK];
@@ -186,19 +188,7 @@ cudaError_t launch_group(const GroupArgs& A, cudaStream_t s) {
     e = cudaFuncSetAttribute(k_group, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)nc);
-  cfg.blockDim = dim3(kGroupThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)nc;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_group, A);
+  return launch_overlapped(k_group, nc, kGroupThreads, nc, smem, s, A);
 }
 
 }  // namespace

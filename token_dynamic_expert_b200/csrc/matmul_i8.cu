@@ -38,6 +38,7 @@
 #include "ace_common.cuh"
 #include "ace_internal.h"
 #include "compact.cuh"
+#include "launch.cuh"
 
 namespace ace {
 namespace {
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(threads_i8(GATHER), 1)
   else
     __syncthreads();
   tc_fence_after();
+  begin_overlapped();
   // the experts' slots and items, two experts a thread
   int total;
   {
@@ -573,22 +575,12 @@ bool map_i8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint
 template <typename TO, bool PAIR, bool GATHER>
 cudaError_t launch_form(const CUtensorMap& w, const CUtensorMap& x, const MatArgs& A, int grid,
                        cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(threads_i8(GATHER));
-  cfg.dynamicSmemBytes = 1024 + kStageRoom;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = PAIR ? 2 : 1;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const size_t smem = 1024 + kStageRoom;
   const cudaError_t e = cudaFuncSetAttribute(
-      k_matmul_i8<TO, PAIR, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+      k_matmul_i8<TO, PAIR, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, k_matmul_i8<TO, PAIR, GATHER>, w, x, A);
+  return launch_overlapped(k_matmul_i8<TO, PAIR, GATHER>, grid, threads_i8(GATHER), PAIR ? 2 : 1,
+                           smem, s, w, x, A);
 }
 
 template <typename TO>
