@@ -62,6 +62,26 @@ def test_norm_sizes(dt, T, d, residual):
     _check_norm(_norm(x, gamma, res), x, gamma, res, dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [8, 100, 264, 512, 520, 1000, 1024])
+def test_many_short_rows(dt, d):
+    """The forms that many rows take: a warp a row, several vectors a thread."""
+    T = 700
+    x, res, gamma = _rand((T, d), dt, d), _rand((T, d), dt, d + 1), torch.rand(d, device="cuda") + 0.5
+    x[13], res[13] = 0, 0
+    x[14, 0] = float("nan")
+    o = _norm(x, gamma, res)
+    ok = torch.arange(T, device="cuda") != 14
+    _check_norm({k: v[ok] for k, v in o.items()}, x[ok], gamma, res[ok], dt)
+    assert (o["q"][14] == 0).all() and o["q_scale"][14].isnan()
+    gu = _rand((T, 2 * d), dt, d + 2, 2.0)
+    _check_swiglu(_swiglu(gu), gu, dt)
+    nv = torch.tensor([401], dtype=torch.int32, device="cuda")
+    o = _swiglu(gu, n_valid=nv)
+    _check_swiglu({k: v[:401] for k, v in o.items()}, gu[:401], dt)
+    assert (o["y"][401:] == 7).all() and (o["q"][401:] == 99).all() and (o["q_scale"][401:] == 7).all()
+
+
 @pytest.mark.parametrize("want", [("sum",), ("y",), ("q",), ("sum", "q"), ("y", "q"), ("sum", "y")])
 def test_norm_each_output_alone(want):
     x, res, gamma = _rand((11, 768), "bf16", 1), _rand((11, 768), "bf16", 2), torch.rand(768, device="cuda")
@@ -182,6 +202,18 @@ def test_swiglu_special_rows():
     _check_swiglu({k: v[1:3] for k, v in o.items()}, gu[1:3], "f32")
     assert (o["q"][[0, 3, 4, 5]] == 0).all()
     assert o["q_scale"][0] == 0 and o["q_scale"][5] == 0 and o["q_scale"][3:5].isnan().all()
+
+
+@pytest.mark.parametrize("m,rows", [(64, 5), (512, 700), (2048, 700)])
+def test_swiglu_from_the_smallest_to_the_largest_rows(m, rows):
+    """Row maxima from 2^-120 to 2^127, each scale in several rows."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    gu = torch.randn(rows, 2 * m, generator=g, device="cuda")
+    gu[:, m:] = torch.tanh(gu[:, m:])
+    e = torch.linspace(-120, 124, rows, device="cuda").round()
+    gu[:, m:] *= torch.ldexp(torch.ones(rows, device="cuda"), e.int())[:, None]
+    gu[:, :m] = gu[:, :m].clamp(-3, 3)
+    _check_swiglu(_swiglu(gu), gu, "f32")
 
 
 def test_rows_replay_in_a_graph_and_on_another_stream():

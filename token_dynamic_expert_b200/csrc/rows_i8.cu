@@ -27,8 +27,10 @@
 namespace ace {
 namespace {
 
+constexpr int kRowWarps = 4;          // rows of a CTA, where a warp holds one
 constexpr int kMaxRow = 16384;        // elements per row
-constexpr float kTinyMax = 7.9e-31f;  // 2^-100: below it 127 / M may overflow, fp64 decides
+constexpr float kTinyMax = 7.9e-31f;  // 2^-100: below it 127 / M may overflow
+constexpr float kHugeMax = 8.5e37f;   // 2^126: above it the fast quotient is 0
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -135,6 +137,13 @@ __device__ __forceinline__ F2 silu_mul(F2 g, F2 u) {
   return mul2(mul2(g, two(s0, s1)), u);
 }
 
+// a / b within 2 ulp, for b below 2^126.
+__device__ __forceinline__ float quotient(float a, float b) {
+  float r;
+  asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // max(m, |a|, |b|) that keeps a NaN of any (m is not negative).
 __device__ __forceinline__ float max_abs(float m, float a, float b) {
   float r;
@@ -176,10 +185,10 @@ struct RowArgs {
 // interval that has to hold no half.
 //   norm:   p 1 rounding, M 1, 127 / M 1, its widening by the interval 1        -> 6
 //   swiglu: h 11 (silu_mul; 1 + e is formed with the factor's product, 1 less);
-//           M 11; 127 / M 1, widening 1                                         -> 24
+//           M 11; 127 / M 2 ulp (4), widening 1                                 -> 28
 template <bool SWIGLU>
 __device__ __forceinline__ constexpr float rel_bound() {
-  return (SWIGLU ? 24.f : 6.f) * 5.9604645e-8f;
+  return (SWIGLU ? 28.f : 6.f) * 5.9604645e-8f;
 }
 
 // 1.5 x 2^23: fmaf(p, inv, kMagic) rounds p inv to the nearest integer (ties to
@@ -205,16 +214,18 @@ __device__ __forceinline__ void load_gamma(const float* gamma, int at, float (&g
   }
 }
 
-// One CTA per row.
-template <typename T, int V, int ITEMS, bool SWIGLU>
-__global__ void __launch_bounds__(V * ITEMS > 16 ? 512 : 1024) k_rows_i8(const RowArgs A) {
+// ONE: a warp a row and kRowWarps rows a CTA, no barrier; else a CTA a row.
+template <typename T, int V, int ITEMS, bool SWIGLU, bool ONE>
+__global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1) k_rows_i8(const RowArgs A) {
   constexpr float kRel = rel_bound<SWIGLU>();
   __shared__ float s_ss[32];
   __shared__ uint32_t s_mx[32];
-  __shared__ unsigned long long s_top;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nt = blockDim.x, nw = nt >> 5;
-  const int64_t row = blockIdx.x;
+  __shared__ unsigned long long s_tops[ONE ? kRowWarps : 1];  // fp64 maxima, as bits
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = ONE ? lane : threadIdx.x;
+  const int nt = ONE ? 32 : blockDim.x, nw = nt >> 5;
+  const int64_t row = ONE ? (int64_t)blockIdx.x * kRowWarps + warp : blockIdx.x;
+  unsigned long long& s_top = s_tops[ONE ? warp : 0];
+  if (ONE && row >= A.rows) return;
   if (A.overlap) begin_overlapped();
   if (SWIGLU && A.n_valid != nullptr && row >= *A.n_valid) return;  // uniform over the row
   const T* a = static_cast<const T*>(A.a) + row * A.lda;
@@ -271,21 +282,24 @@ __global__ void __launch_bounds__(V * ITEMS > 16 ? 512 : 1024) k_rows_i8(const R
   // the bits of non-negative floats order like the values, NaN above infinity
   uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx) & 0x7fffffffu);
   if (!SWIGLU) ss = warp_sum(ss);
-  if (lane == 0) {
-    s_mx[warp] = mb;
-    if (!SWIGLU) s_ss[warp] = ss;
+  if (!ONE) {
+    if (lane == 0) {
+      s_mx[warp] = mb;
+      if (!SWIGLU) s_ss[warp] = ss;
+    }
+    __syncthreads();
+    mb = __reduce_max_sync(0xffffffffu, lane < nw ? s_mx[lane] : 0u);
+    if (!SWIGLU) ss = warp_sum(lane < nw ? s_ss[lane] : 0.f);
   }
-  __syncthreads();
-  mb = __reduce_max_sync(0xffffffffu, lane < nw ? s_mx[lane] : 0u);
-  if (!SWIGLU) ss = warp_sum(lane < nw ? s_ss[lane] : 0.f);
   const float r = SWIGLU ? 1.f : 1.0f / sqrtf(ss / (float)d + A.eps);
   const float M = __uint_as_float(mb);
   const bool finite = isfinite(M) && (SWIGLU || isfinite(ss));
   const bool usable = finite && M >= 1.17549435e-38f;  // else no element to scale by: q = 0
-  const bool tiny = M < kTinyMax;
-  const float inv = usable && !tiny ? __fdiv_rn(127.f, M) : 0.f;
+  const bool far = M < kTinyMax || M > kHugeMax;  // 127 / M in fp32 is no use: fp64 decides all
+  // (the exact division costs SwiGLU 1 us of 36 at 65536 rows of 512)
+  const float inv = !usable || far ? 0.f : SWIGLU ? quotient(127.f, M) : __fdiv_rn(127.f, M);
   const float inv_lo = inv * (1.f - kRel), inv_hi = inv * (1.f + kRel);
-  uint32_t differ = usable && tiny ? 1u : 0u;
+  uint32_t differ = usable && far ? 1u : 0u;
 
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(V * ITEMS > 16 ? 512 : 1024) k_rows_i8(const R
   if (A.q == nullptr) return;
   if (tid == 0)
     A.q_scale[row] = usable ? M * (r * (1.f / 127.f)) : finite ? 0.f : __uint_as_float(0x7fc00000u);
-  if (!__syncthreads_or((int)differ)) return;
+  if (ONE ? !__any_sync(0xffffffffu, differ != 0u) : !__syncthreads_or((int)differ)) return;
 
   // fp64: first M, from the elements that fp32 cannot tell from the largest
   const float cand = M * (1.f - 4.f * kRel);
@@ -332,7 +346,10 @@ __global__ void __launch_bounds__(V * ITEMS > 16 ? 512 : 1024) k_rows_i8(const R
                               fabs(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU))));
     }
   }
-  __syncthreads();
+  if (ONE)
+    __syncwarp();
+  else
+    __syncthreads();
   const double top = __longlong_as_double((long long)s_top);
   if (differ == 0u) return;
 #pragma unroll
@@ -342,7 +359,7 @@ __global__ void __launch_bounds__(V * ITEMS > 16 ? 512 : 1024) k_rows_i8(const R
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       const float p = SWIGLU ? v[i][c] : v[i][c] * A.gamma[at * V + c];
-      if (tiny || fmaf(p, inv_lo, kMagic) != fmaf(p, inv_hi, kMagic))
+      if (far || fmaf(p, inv_lo, kMagic) != fmaf(p, inv_hi, kMagic))
         A.q[row * A.ldq + at * V + c] =
             (int8_t)quotient64(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU), top);
     }
@@ -350,36 +367,50 @@ __global__ void __launch_bounds__(V * ITEMS > 16 ? 512 : 1024) k_rows_i8(const R
 }
 
 template <typename T, int V, int ITEMS, bool SWIGLU>
-cudaError_t launch_items(const RowArgs& A, cudaStream_t s) {
+cudaError_t launch_cta(const RowArgs& A, cudaStream_t s) {
   const int threads = cdiv(cdiv(cdiv(A.d, V), ITEMS), 32) * 32;
+  auto kernel = k_rows_i8<T, V, ITEMS, SWIGLU, false>;
   // Few rows may start while the kernel before ends (3.0 -> 2.7 us for 61 rows of
   // SwiGLU).  With many, a wait in each of the small CTAs costs more than the
   // launch (65536 rows: 51 -> 81 us).
-  if (A.overlap)
-    return launch_overlapped(k_rows_i8<T, V, ITEMS, SWIGLU>, (unsigned)A.rows, threads, 1, 0, s, A);
-  k_rows_i8<T, V, ITEMS, SWIGLU><<<(unsigned)A.rows, threads, 0, s>>>(A);
+  if (A.overlap) return launch_overlapped(kernel, (unsigned)A.rows, threads, 1, 0, s, A);
+  kernel<<<(unsigned)A.rows, threads, 0, s>>>(A);
   return cudaGetLastError();
 }
 
-// Vectors per thread.  Few rows: one, the shortest chain (2.3 us against 2.6
-// with two, one row of 2048).  Many rows: two of 16 bytes, enough loads in
-// flight with little work per row besides them (8191 rows of 2048 bf16: 1, 2,
-// 4, 8 vectors 35, 28, 31, 39 us); eight narrower ones (4000 rows of 2050: 8
-// and 16 of them 25 and 34 us).  SwiGLU's bf16 rows are bound by arithmetic and
-// take one (65536 rows of 512: 1 and 2 vectors 41.8 and 45 us).  More where a
-// row needs more than 1024 threads.
+template <typename T, int V, int ITEMS, bool SWIGLU>
+cudaError_t launch_warp(const RowArgs& A, cudaStream_t s) {
+  k_rows_i8<T, V, ITEMS, SWIGLU, true>
+      <<<(unsigned)cdiv(A.rows, kRowWarps), 32 * kRowWarps, 0, s>>>(A);
+  return cudaGetLastError();
+}
+
+// Vectors per thread, and whether a warp or a CTA holds a row.
+//   few rows: one vector, the shortest chain (2.3 us against 2.6 with two, one row
+//   of 2048)
+//   many rows of up to 128 16-byte vectors: a warp, since the work per row besides
+//   its elements would be most of a CTA's (65536 rows of 512, SwiGLU, bf16: 41 ->
+//   35 us; 32768 of 1024: 41 -> 36; norm of 21845 rows of 768: 34 -> 30)
+//   longer ones: two 16-byte vectors a thread, enough loads in flight and little
+//   besides the elements (8191 rows of 2048, norm, bf16: 1, 2, 4, 8 vectors 35, 28,
+//   31, 39 us; 16384 rows of 2048, SwiGLU: 1, 2 vectors 43, 33 us)
+//   narrower vectors: eight (4000 rows of 2050: 8 and 16 of them 25 and 34 us)
+// More where a row needs more than 1024 threads.
 template <typename T, int V, bool SWIGLU>
 cudaError_t launch_v(const RowArgs& A, cudaStream_t s) {
   const int nv = cdiv(A.d, V);
   if constexpr (V >= 4) {
-    const int items = A.overlap || (SWIGLU && V == 8) ? 1 : 2;
-    if (items == 1 && nv <= 1024) return launch_items<T, V, 1, SWIGLU>(A, s);
-    if (nv <= 2048) return launch_items<T, V, 2, SWIGLU>(A, s);
-    if constexpr (V == 4) return launch_items<T, V, 4, SWIGLU>(A, s);
+    if (!A.overlap && nv <= 32) return launch_warp<T, V, 1, SWIGLU>(A, s);
+    if (!A.overlap && nv <= 64) return launch_warp<T, V, 2, SWIGLU>(A, s);
+    if (!A.overlap && nv <= 128) return launch_warp<T, V, 4, SWIGLU>(A, s);
+    const int items = A.overlap ? 1 : 2;
+    if (items == 1 && nv <= 1024) return launch_cta<T, V, 1, SWIGLU>(A, s);
+    if (nv <= 2048) return launch_cta<T, V, 2, SWIGLU>(A, s);
+    if constexpr (V == 4) return launch_cta<T, V, 4, SWIGLU>(A, s);
   } else {
-    if (A.overlap && nv <= 1024) return launch_items<T, V, 1, SWIGLU>(A, s);
-    if (nv <= 8192) return launch_items<T, V, 8, SWIGLU>(A, s);
-    if constexpr (V == 1) return launch_items<T, V, 16, SWIGLU>(A, s);
+    if (A.overlap && nv <= 1024) return launch_cta<T, V, 1, SWIGLU>(A, s);
+    if (nv <= 8192) return launch_cta<T, V, 8, SWIGLU>(A, s);
+    if constexpr (V == 1) return launch_cta<T, V, 16, SWIGLU>(A, s);
   }
   return cudaErrorInvalidValue;  // not reached: d <= kMaxRow
 }
