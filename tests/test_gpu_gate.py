@@ -98,6 +98,21 @@ def test_scores_closer_than_fp32_can_tell(score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_chains_of_equal_and_nearly_equal_scores_across_the_border(score):
+    """A few distinct values, an fp32 step or less apart in their choice value, each
+    held by several experts: ties and near ties on both sides of rank k."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    E, T = 48, 400
+    which = torch.randint(0, 6, (T, E), generator=g, device="cuda")
+    x = torch.tensor([0.5, 0.5 + 2.0 ** -23, 0.5 + 2.0 ** -22, 0.5 - 2.0 ** -24, 0.25, -1.0], device="cuda")[which]
+    x[:, 40:] -= 3
+    for bias in (torch.zeros(E, device="cuda"), (torch.arange(E, device="cuda") % 3) * 2.0 ** -25):
+        for k in (1, 2, 5, 8, 16):
+            _check(x, k, bias, score=score)
+            _check(x, min(k, 12), bias, score=score, n_groups=4, topk_groups=2, group_score="top2")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("lowest", [-float("inf"), torch.finfo(torch.float32).min])
 def test_masked_experts(score, biased, lowest):

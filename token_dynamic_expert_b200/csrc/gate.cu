@@ -325,16 +325,17 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
           }
         }
 
-  // How far two exact scores may lie apart where fp32 sees them equal, each in
-  // half steps (2^-24) of the scores' scale:
-  //   sigmoid: e^-x by ex2.approx 4 and its argument's rounding |x|, which change
-  //   s by their s (1 - s) fold, 1 + 0.23; 1 + e and the reciprocal 3: under 5
-  //   softmax, scale 1 / z: the exponent's roundings 2 d 2^-d..., under 1, ex2 4,
-  //   two products 2; the sum's terms likewise and its at most 32 + 5 additions:
-  //   under 64
-  // and the addition of the bias, half a step of c.  Twice for two scores, and
-  // again as room.
-  const float err = SIG ? 9.6e-7f : 1.1e-5f * inv_z;
+  // Bound on the fp32 error of a score that decides, u = 2^-24:
+  //   sigmoid: e^-x has the relative error of its argument's rounding and of
+  //   log2 e, 1.22 |x| u, and of ex2.approx, 4 u; s moves by s (1 - s) of that, at
+  //   most (0.28 + 1) u; 1 + e 1 u, rcp.approx 2 u: 4.3 u
+  //   softmax, in units of the largest score 1 / z: the exponent d = m - x 2.22 d u
+  //   and ex2.approx 4 u, of e^-d: 4.9 u; z the same, weighted (d is 6.3 on average
+  //   at most), and its 36 additions: 54 u; 1 / z and the product 2 u: 61 u
+  // A choice value adds the rounding of the bias, u |c|, a group's sum that of two
+  // values and its own.  Two values that differ by less than twice the bound, with a
+  // quarter to spare, are compared in fp64.
+  const float err = SIG ? 3.8e-7f : 4.6e-6f * inv_z;
   bool near = false;
 
   if (A.G > 1) {
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
       const uint32_t next = __reduce_max_sync(0xffffffffu, !allowed && L.group < A.G ? gk : 0u);
       const float top = __uint_as_float(
           __reduce_max_sync(0xffffffffu, L.group < A.G ? __float_as_uint(mag) : 0u));
-      near = next != 0u && fkey_inv(last) - fkey_inv(next) <= 2.f * (err + 4.8e-7f * top);
+      near = next != 0u && fkey_inv(last) - fkey_inv(next) <= 2.f * (2.f * err + 1.5e-7f * top);
     }
     if (!allowed) c[0] = 0ull;
   }
@@ -408,15 +409,16 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     const float nx = __shfl_down_sync(0xffffffffu, my_x, 1);
     const float nb = __shfl_down_sync(0xffffffffu, my_b, 1);
     const float nvv = fkey_inv(nk);
-    const bool same = nx == my_x && nb == my_b;  // a true tie: the index decides
-    if (lane <= A.k && nk != 0u && !same &&
-        v - nvv <= 2.f * (err + 1.2e-7f * fmaxf(fabsf(v), fabsf(nvv)))) {
-      close = lane < A.k;
-      near |= lane == A.k;  // the one behind the border is in question too
-    }
+    const bool next = lane <= A.k && nk != 0u;
+    const bool same = next && nx == my_x && nb == my_b;  // a true tie: the index decides
+    const bool touch = next && !same &&
+                       v - nvv <= 2.f * (err + 7.5e-8f * fmaxf(fabsf(v), fabsf(nvv)));
+    // ranks i and i + 1 that touch; the first k + 1 experts settle it among themselves
+    // unless equal or touching ones lead on behind them
+    close = (__ballot_sync(0xffffffffu, touch) & ((1u << A.k) - 1u)) != 0u;
+    near |= ((__ballot_sync(0xffffffffu, touch || same) >> (A.k - 1)) & 3u) == 3u;
   }
   const bool all64 = __any_sync(0xffffffffu, near);
-  close = BIAS && __any_sync(0xffffffffu, close);
   if (all64)
     my_e = choose64<TL, NV>(A, row, lane, lg);
   else if (close)
