@@ -58,6 +58,19 @@ def test_dense_large_odd():
     _check(4099, 4097, 272, out="f32")
 
 
+@pytest.mark.parametrize("S,N,K", [(4100, 4000, 1056), (4096, 4096, 1024), (4000, 4097, 1168)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_dense_large(S, N, K, out):
+    _check(S, N, K, out=out)
+
+
+@pytest.mark.parametrize("S,N,K,E", [(33000, 1030, 1040, 100), (40000, 768, 1024, 37), (70000, 300, 1152, 7),
+                                     (30000, 1024, 3200, 256)])
+@pytest.mark.parametrize("rows,gate", [(None, True), (900, False)])
+def test_grouped_large(S, N, K, E, rows, gate):
+    _check(S, N, K, E, rows=rows, gate=gate, used=S - 5)
+
+
 @pytest.mark.parametrize("S,N,K,E", [(1, 128, 128, 4), (64, 1536, 512, 128), (61, 100, 144, 7), (500, 257, 256, 3),
                                      (3000, 384, 336, 64), (777, 96, 64, 512), (5000, 512, 128, 2)])
 @pytest.mark.parametrize("rows,gate", [(None, False), (None, True), (97, False), (1, True)])

@@ -31,6 +31,9 @@
 //                1, 4, 8 warps 591, 180, 172 us)
 // Two TMEM accumulators alternate between items, so an epilogue overlaps the
 // next main loop.  All waits are bounded.
+// A gather warp without rows in an item passes it over, and begins an item only
+// once the weights' warp has: the ring's barriers tell one turn from the next, not
+// from the one after.
 #include <math.h>
 
 #include <atomic>
@@ -80,6 +83,7 @@ struct SmemI8 {
   int s_warp[32];
   uint32_t tmem;
   int abort_flag;
+  int item;  // the last item the weights' warp has begun
 };
 
 __host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
@@ -255,6 +259,25 @@ __device__ __forceinline__ Item item_at(const SmemI8& sm, const MatArgs& A, int 
   return {lo, sm.first[lo] + q * each, max(0, min(each, cnt - q * each)), l / ntile};
 }
 
+// Bounded wait until the weights' warp has begun item w.
+__device__ __forceinline__ bool wait_item(const SmemI8& sm, int w, uint32_t* status,
+                                          volatile int* abort_flag) {
+  const volatile int* item = &sm.item;
+  if (*item < w) {
+    const uint64_t t0 = global_ns();
+    while (*item < w) {
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        raise_flag(status, ACE_FLAG_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  __threadfence_block();
+  return true;
+}
+
 // GATHER: the slots' rows come through row_of.
 template <typename TO, bool PAIR, bool GATHER>
 __global__ void __launch_bounds__(threads_i8(GATHER), 1)
@@ -287,6 +310,7 @@ __global__ void __launch_bounds__(threads_i8(GATHER), 1)
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
+    sm.item = -1;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
@@ -352,6 +376,10 @@ __global__ void __launch_bounds__(threads_i8(GATHER), 1)
     int stage = 0;
     uint32_t phase = 0;
     for (int w = w0; w < total && !*abort_flag; w += nw) {
+      if (GATHER && lane == 0) {
+        __threadfence_block();
+        *static_cast<volatile int*>(&sm.item) = w;
+      }
       const Item it = item_at<PAIR>(sm, A, nblk, w);
       const int half = it.half<PAIR>(), row = it.row0 + (int)rank * half;
       const int nbox = (half + A.box - 1) / A.box;
@@ -391,7 +419,15 @@ __global__ void __launch_bounds__(threads_i8(GATHER), 1)
       uint32_t phase = 0;
       for (int w = w0; w < total && !*abort_flag; w += nw) {
         const Item it = item_at<PAIR>(sm, A, nblk, w);
-        const bool mine = lane < kPer && g < it.groups<PAIR>((int)rank);
+        const int ng = it.groups<PAIR>((int)rank);
+        const bool mine = lane < kPer && g < ng;
+        if (g - lane >= ng) {  // the same for the warp
+          const int next = stage + ksteps;
+          phase ^= (uint32_t)(next / NS) & 1u;
+          stage = next % NS;
+          continue;
+        }
+        if (!wait_item(sm, w, A.status, abort_flag)) break;
         int rows[4] = {0, 0, 0, 0};
         if (mine)
 #pragma unroll
