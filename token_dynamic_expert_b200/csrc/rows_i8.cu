@@ -40,8 +40,9 @@ struct alignas(sizeof(T) * V) Vec {
 };
 
 // Two fp32 values in a register pair.  Blackwell's f32x2 instructions work on
-// both at once; these kernels are bound by instruction issue before HBM, and
-// the pairs halve their arithmetic.
+// both at once, which halves the arithmetic of SwiGLU's exponential (41 against 45
+// us at 65536 rows of 512 when it came); the norm's few operations lost more to
+// pairing registers than they gained.
 typedef unsigned long long F2;
 __device__ __forceinline__ F2 two(float a, float b) {
   F2 r;
@@ -120,7 +121,8 @@ __device__ __forceinline__ Vec<int8_t, V> low_bytes(const uint32_t (&w)[V]) {
 
 // silu(g) u of a pair.  e^-g = 2^y with y = -g log2 e: the product's rounding
 // and the constant's are formed exactly enough (r) and put back as a factor
-// 1 + r ln 2, since 2^(y + r) = 2^y (1 + r ln 2 + ...) and |r| < 2^-16.
+// 1 + r ln 2, since 2^(y + r) = 2^y (1 + r ln 2 + ...) and |r| < 2^-16 where e^-g is
+// neither 0 nor infinite.
 // Relative error in half steps: ex2.approx 4, the factor 1 and its product 1,
 // 1 + e 1, rcp.approx 2, the two products 2: 11.  Above g = 128 e^-g is far
 // below half a step of 1; below g = -126 ln 2 the reciprocal underflows and
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1) k_rows_i8(cons
   if (ONE ? !__any_sync(0xffffffffu, differ != 0u) : !__syncthreads_or((int)differ)) return;
 
   // fp64: first M, from the elements that fp32 cannot tell from the largest
+  if (ONE) __syncwarp();  // s_top is 0 for every lane
   const float cand = M * (1.f - 4.f * kRel);
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
