@@ -46,7 +46,7 @@
 namespace ace {
 namespace {
 
-constexpr int kM = 128;            // weight rows per item
+constexpr int kM = 128;            // weight rows a CTA holds
 constexpr int kStepK = 128;        // bytes of K per stage: one swizzle row
 constexpr int kWBytes = kM * kStepK;
 constexpr int kMaxN = 256;         // slots per tile
