@@ -490,7 +490,8 @@ ACE_API ace_status ace_add_rmsnorm(const void* x, int64_t ldx, const void* resid
  * ace_moe_logits -- the router's logits on their own, for gates that
  *   ace_moe_forward does not form (ace_gate_topk):
  *     logits[t][e] = RMSNorm(u_t) gamma . w_e (+ router_bias[e])
- *   by ace_moe_forward's kernels, the same bits.  u (device) [T][d]
+ *   at the forward's accuracy: for more than 8 tokens by its prefill kernels, the
+ *   same bits; up to 8 tokens in one launch with fp32 sums.  u (device) [T][d]
  *   layer->dtype, 16-byte aligned; logits (device) [T][E] fp32.  Of the layer
  *   only d, E, dtype, gamma, w_router and router_bias are read (m and k have
  *   to pass the layer checks).  Device flags: ace_read_status on ws.

@@ -189,6 +189,32 @@ def test_logits_are_the_forwards():
         assert torch.equal(logits, dbg.logits)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,bias", [(1, 64, 1, False), (1, 2048, 128, True), (2, 192, 9, True), (5, 1088, 60, False),
+                                        (7, 320, 256, True), (8, 2048, 512, False), (8, 4096, 33, True), (9, 2048, 33, True)])
+def test_logits_of_few_tokens(dtype, T, d, E, bias):
+    """fp32 products and sums: at most d / 32 in a lane, 5 across the warp (8 tokens
+    of 4096 and 9 tokens take the prefill's way, whose sums run over 64 columns and
+    then d / 64 chunks); x has 3 roundings and the root's (d / 32 + 8 half steps, halved)."""
+    from token_dynamic_expert_b200 import ace
+    g = torch.Generator(device="cuda").manual_seed(d + E)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    u = torch.randn(T, d, generator=g, device="cuda").to(dt)
+    wr = (torch.randn(E, d, generator=g, device="cuda") * 0.05).to(dt)
+    gamma, b = torch.rand(d, generator=g, device="cuda") + 0.5, torch.randn(E, generator=g, device="cuda") if bias else None
+    R = ace.make_router_layer(gamma, wr, b)
+    ws = ace.alloc_workspace(ace.ace_logits_workspace_size(R, T))
+    ws.fill_(0xAB)
+    logits = torch.full((T, E), 7.0, device="cuda")
+    ace.ace_moe_logits(R, u, logits, ws, eps_rms=1e-5)
+    assert ace.ace_read_status(ws) == (ace.ACE_OK, 0)
+    x = ora.f64(u) / np.sqrt((ora.f64(u) ** 2).mean(1, keepdims=True) + 1e-5) * ora.f64(gamma)
+    ref, mag = x @ ora.f64(wr).T, np.abs(x) @ np.abs(ora.f64(wr)).T
+    if bias:
+        ref, mag = ref + ora.f64(b), mag + np.abs(ora.f64(b))
+    assert (np.abs(ora.f64(logits) - ref) <= (d / 32 + 40) * ora.U32 * mag).all()
+
+
 def test_refusals():
     from token_dynamic_expert_b200 import layer_i8
     L, u, _ = _make(8, 128, 8, 64, 2)

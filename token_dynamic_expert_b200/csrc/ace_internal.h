@@ -69,11 +69,12 @@ ace_status check_fusion(const ace_layer& L, int fusion);
 // ---------------------------------------------------------------- launchers
 // 1/rms per token, x (nullable); zeroes clear[0 .. n_clear) (n_clear <= 256)
 // and zero[0 .. n_zero); w3 (nullable, bf16 layers): gamma (.) w_router as
-// three bf16 terms [3][E][d]
+// three bf16 terms [3][E][d]; min_ctas: CTAs beyond the tokens' own, which share in
+// forming w3
 cudaError_t launch_rmsnorm(ace_dtype dt, const void* u, int T, int d, const float* gamma,
                            float eps, float* inv_rms, void* x, uint32_t* clear, int n_clear,
                            uint32_t* zero, size_t n_zero, const void* wr, int E, void* w3,
-                           cudaStream_t s);
+                           cudaStream_t s, int min_ctas = 0);
 // Tensor-core router (bf16 layers): part[split][t][e] from u [T][d] (bf16),
 // 1/rms and the three-term router operand w3 [3][E][d].
 int router_tc_splits(int T, int d, int E, int num_sms);
@@ -83,6 +84,11 @@ cudaError_t launch_router_tc(const void* u, const float* inv_rms, const void* w3
 cudaError_t launch_router_logits(ace_dtype dt, const void* u, const float* inv_rms,
                                  const float* gamma, const void* wr, int T, int d, int E,
                                  int splitk, float* part, cudaStream_t s);
+// logits [T][E] of few tokens in one launch, and whether it takes them
+bool logits_few_fits(int T, int d);
+cudaError_t launch_logits_few(ace_dtype dt, const void* u, int T, int d, const float* gamma,
+                              float eps, const void* wr, const float* bias, int E, float* logits,
+                              uint32_t* status, cudaStream_t s);
 // logits [T][E] from the partial sums part [splitk][T][E] (+ bias [E] or NULL)
 cudaError_t launch_sum_splits(const float* part, int splitk, int T, int E, const float* bias,
                               float* logits, int num_sms, cudaStream_t s);

@@ -22,6 +22,7 @@
 #include "ace_common.cuh"
 #include "ace_internal.h"
 #include "compact.cuh"
+#include "launch.cuh"
 
 namespace ace {
 
@@ -107,8 +108,8 @@ __global__ void __launch_bounds__(256) k_rmsnorm(const T* __restrict__ u, int Tn
 cudaError_t launch_rmsnorm(ace_dtype dt, const void* u, int T, int d, const float* gamma,
                            float eps, float* inv_rms, void* x, uint32_t* clear, int n_clear,
                            uint32_t* zero, size_t n_zero, const void* wr, int E, void* w3,
-                           cudaStream_t s) {
-  dim3 grid(cdiv(T, 8));
+                           cudaStream_t s, int min_ctas) {
+  dim3 grid(cdiv(T, 8) > min_ctas ? cdiv(T, 8) : min_ctas);
   if (n_clear > 256) return cudaErrorInvalidValue;
   if (dt == ACE_BF16)
     k_rmsnorm<__nv_bfloat16><<<grid, 256, 0, s>>>(
@@ -178,6 +179,95 @@ __global__ void __launch_bounds__(256) k_router_logits(const T* __restrict__ u,
       if (e < E) out[(size_t)t * E + e] = acc[i][j];
     }
   }
+}
+
+// Logits of a decode step's tokens (Tn <= kDecodeMaxT) in one launch: every CTA
+// forms the tokens' x = xhat(u, 1/rms, gamma) in shared memory, a warp a token, then
+// each of its warps takes one expert's row against all of them in fp32 (a lane's
+// sums, then the warp's).  Bound by latency: two loads one after the other.  The
+// prefill's way would fold gamma into the router's rows first, for a handful of
+// tokens.
+template <typename T>
+__global__ void __launch_bounds__(256) k_logits_few(const T* __restrict__ u, int Tn, int d,
+                                                    const float* __restrict__ gamma, float eps,
+                                                    const T* __restrict__ wr,
+                                                    const float* __restrict__ bias, int E,
+                                                    float* __restrict__ logits, uint32_t* status) {
+  extern __shared__ float s_x[];  // [Tn][d]
+  constexpr int V = 16 / (int)sizeof(T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nv = d / V;
+  begin_overlapped();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
+  if (warp < Tn) {
+    const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)warp * d);
+    float ss = 0.f;
+    for (int v = lane; v < nv; v += 32) {
+      const uint4 q = ur[v];
+      const T* e = reinterpret_cast<const T*>(&q);
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float f = to_f(e[c]);
+        ss = fmaf(f, f, ss);
+        s_x[warp * d + v * V + c] = f;
+      }
+    }
+    const float r = 1.0f / sqrtf(warp_sum(ss) / (float)d + eps);
+    for (int v = lane; v < nv; v += 32)  // the lane's own elements
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const int i = v * V + c;
+        s_x[warp * d + i] = xhat(s_x[warp * d + i], r, gamma[i]);
+      }
+  }
+  __syncthreads();
+  const int e = blockIdx.x * 8 + warp;
+  if (e >= E) return;
+  float acc[kDecodeMaxT];
+#pragma unroll
+  for (int t = 0; t < kDecodeMaxT; ++t) acc[t] = 0.f;
+  const uint4* w = reinterpret_cast<const uint4*>(wr + (size_t)e * d);
+#pragma unroll 4
+  for (int v = lane; v < nv; v += 32) {
+    const uint4 q = w[v];
+    const T* we = reinterpret_cast<const T*>(&q);
+#pragma unroll
+    for (int t = 0; t < kDecodeMaxT; ++t) {
+      if (t >= Tn) break;
+#pragma unroll
+      for (int c = 0; c < V; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(s_x + t * d + v * V + c);
+        acc[t] = fmaf(x.x, to_f(we[c]), acc[t]);
+        acc[t] = fmaf(x.y, to_f(we[c + 1]), acc[t]);
+        acc[t] = fmaf(x.z, to_f(we[c + 2]), acc[t]);
+        acc[t] = fmaf(x.w, to_f(we[c + 3]), acc[t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kDecodeMaxT; ++t) {
+    if (t >= Tn) break;
+    const float v = warp_sum(acc[t]);
+    if (lane == 0) logits[(size_t)t * E + e] = bias ? v + bias[e] : v;
+  }
+}
+
+bool logits_few_fits(int T, int d) { return T <= kDecodeMaxT && (size_t)T * d * 4 <= 96 * 1024; }
+
+cudaError_t launch_logits_few(ace_dtype dt, const void* u, int T, int d, const float* gamma,
+                              float eps, const void* wr, const float* bias, int E, float* logits,
+                              uint32_t* status, cudaStream_t s) {
+  const size_t smem = (size_t)T * d * 4;
+  const unsigned grid = (unsigned)cdiv(E, 8);
+  auto go = [&](auto kernel, auto* up, auto* wp) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kernel, grid, 256, 1, smem, s, up, T, d, gamma, eps, wp, bias, E, logits,
+                             status);
+  };
+  if (dt == ACE_BF16)
+    return go(k_logits_few<__nv_bfloat16>, (const __nv_bfloat16*)u, (const __nv_bfloat16*)wr);
+  return go(k_logits_few<float>, (const float*)u, (const float*)wr);
 }
 
 // logits[i] = the split-K partial sums of element i in split order (+ bias), as
