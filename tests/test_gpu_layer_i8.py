@@ -193,9 +193,9 @@ def test_logits_are_the_forwards():
 @pytest.mark.parametrize("T,d,E,bias", [(1, 64, 1, False), (1, 2048, 128, True), (2, 192, 9, True), (5, 1088, 60, False),
                                         (7, 320, 256, True), (8, 2048, 512, False), (8, 4096, 33, True), (9, 2048, 33, True)])
 def test_logits_of_few_tokens(dtype, T, d, E, bias):
-    """fp32 products and sums: at most d / 32 in a lane, 5 across the warp (8 tokens
-    of 4096 and 9 tokens take the prefill's way, whose sums run over 64 columns and
-    then d / 64 chunks); x has 3 roundings and the root's (d / 32 + 8 half steps, halved)."""
+    """fp32 products and sums: gamma w 1 rounding, at most d / 256 vectors of 8 in a
+    thread, 5 across the warp, 8 across the CTA; the root's sum likewise, halved (9
+    tokens take the prefill's way, sums of 64 columns and then d / 64 chunks)."""
     from token_dynamic_expert_b200 import ace
     g = torch.Generator(device="cuda").manual_seed(d + E)
     dt = torch.bfloat16 if dtype == "bf16" else torch.float32

@@ -525,8 +525,8 @@ ace_status ace_moe_logits(const ace_layer* layer, const void* u, int T, float ep
     return ACE_OK;
   }
   // up to 8 tokens in one launch: the 8-bit layer of one token (d = 2048, E = 256)
-  // takes 41 us with it and took 208 with the prefill's three
-  if (logits_few_fits(T, L.d)) {
+  // takes 36 us with it and took 208 with the prefill's three
+  if (T <= kDecodeMaxT) {
     ACE_CK(launch_logits_few(L.dtype, u, T, L.d, L.gamma, eps_rms, L.w_router, L.router_bias, L.E,
                              logits, at<uint32_t>(ws, ly.status), s));
     return ACE_OK;

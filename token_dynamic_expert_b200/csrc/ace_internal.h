@@ -84,8 +84,7 @@ cudaError_t launch_router_tc(const void* u, const float* inv_rms, const void* w3
 cudaError_t launch_router_logits(ace_dtype dt, const void* u, const float* inv_rms,
                                  const float* gamma, const void* wr, int T, int d, int E,
                                  int splitk, float* part, cudaStream_t s);
-// logits [T][E] of few tokens in one launch, and whether it takes them
-bool logits_few_fits(int T, int d);
+// logits [T][E] of up to kDecodeMaxT tokens in one launch
 cudaError_t launch_logits_few(ace_dtype dt, const void* u, int T, int d, const float* gamma,
                               float eps, const void* wr, const float* bias, int E, float* logits,
                               uint32_t* status, cudaStream_t s);

@@ -181,93 +181,93 @@ __global__ void __launch_bounds__(256) k_router_logits(const T* __restrict__ u,
   }
 }
 
-// Logits of a decode step's tokens (Tn <= kDecodeMaxT) in one launch: every CTA
-// forms the tokens' x = xhat(u, 1/rms, gamma) in shared memory, a warp a token, then
-// each of its warps takes one expert's row against all of them in fp32 (a lane's
-// sums, then the warp's).  Bound by latency: two loads one after the other.  The
-// prefill's way would fold gamma into the router's rows first, for a handful of
-// tokens.
+// Logits of a decode step's tokens (Tn <= kDecodeMaxT) in one launch: a CTA takes
+// kFewExperts rows of the router against every token, its threads 16-byte vectors
+// of the hidden size.  As the tensor-core router, l = r_t sum_k u_tk (gamma_k w_ek)
+// with gamma w rounded once; r_t comes from the same pass.  fp32 sums: a thread's,
+// the warp's, then the CTA's.  Bound by latency: one round of loads, one reduction
+// (4 to 6 us; a warp an expert over normalised rows in shared memory took 11 and 20
+// us for 1 and 8 tokens of 2048 x 128).
+constexpr int kFewExperts = 2;
+
 template <typename T>
 __global__ void __launch_bounds__(256) k_logits_few(const T* __restrict__ u, int Tn, int d,
                                                     const float* __restrict__ gamma, float eps,
                                                     const T* __restrict__ wr,
                                                     const float* __restrict__ bias, int E,
                                                     float* __restrict__ logits, uint32_t* status) {
-  extern __shared__ float s_x[];  // [Tn][d]
-  constexpr int V = 16 / (int)sizeof(T);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nv = d / V;
+  constexpr int V = 16 / (int)sizeof(T), N = 1 + kFewExperts;
+  __shared__ float s_part[8][kDecodeMaxT * N];  // a warp's sums: u^2, then a sum an expert
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nv = d / V;
+  const int e0 = blockIdx.x * kFewExperts;
   begin_overlapped();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
-  if (warp < Tn) {
-    const uint4* ur = reinterpret_cast<const uint4*>(u + (size_t)warp * d);
-    float ss = 0.f;
-    for (int v = lane; v < nv; v += 32) {
-      const uint4 q = ur[v];
-      const T* e = reinterpret_cast<const T*>(&q);
+  if (blockIdx.x == 0 && tid == 0) *status = 0u;
+  float acc[kDecodeMaxT][N];
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float f = to_f(e[c]);
-        ss = fmaf(f, f, ss);
-        s_x[warp * d + v * V + c] = f;
-      }
+  for (int t = 0; t < kDecodeMaxT; ++t)
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[t][j] = 0.f;
+  for (int v = tid; v < nv; v += 256) {
+    uint4 w[kFewExperts], x[kDecodeMaxT];
+#pragma unroll
+    for (int j = 0; j < kFewExperts; ++j)
+      w[j] = reinterpret_cast<const uint4*>(wr + (size_t)min(e0 + j, E - 1) * d)[v];
+#pragma unroll
+    for (int t = 0; t < kDecodeMaxT; ++t)
+      if (t < Tn) x[t] = reinterpret_cast<const uint4*>(u + (size_t)t * d)[v];
+    float gw[kFewExperts][V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      const float g = gamma[v * V + c];
+#pragma unroll
+      for (int j = 0; j < kFewExperts; ++j)
+        gw[j][c] = __fmul_rn(g, to_f(reinterpret_cast<const T*>(&w[j])[c]));
     }
-    const float r = 1.0f / sqrtf(warp_sum(ss) / (float)d + eps);
-    for (int v = lane; v < nv; v += 32)  // the lane's own elements
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const int i = v * V + c;
-        s_x[warp * d + i] = xhat(s_x[warp * d + i], r, gamma[i]);
-      }
-  }
-  __syncthreads();
-  const int e = blockIdx.x * 8 + warp;
-  if (e >= E) return;
-  float acc[kDecodeMaxT];
-#pragma unroll
-  for (int t = 0; t < kDecodeMaxT; ++t) acc[t] = 0.f;
-  const uint4* w = reinterpret_cast<const uint4*>(wr + (size_t)e * d);
-#pragma unroll 4
-  for (int v = lane; v < nv; v += 32) {
-    const uint4 q = w[v];
-    const T* we = reinterpret_cast<const T*>(&q);
 #pragma unroll
     for (int t = 0; t < kDecodeMaxT; ++t) {
       if (t >= Tn) break;
 #pragma unroll
-      for (int c = 0; c < V; c += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(s_x + t * d + v * V + c);
-        acc[t] = fmaf(x.x, to_f(we[c]), acc[t]);
-        acc[t] = fmaf(x.y, to_f(we[c + 1]), acc[t]);
-        acc[t] = fmaf(x.z, to_f(we[c + 2]), acc[t]);
-        acc[t] = fmaf(x.w, to_f(we[c + 3]), acc[t]);
+      for (int c = 0; c < V; ++c) {
+        const float f = to_f(reinterpret_cast<const T*>(&x[t])[c]);
+        acc[t][0] = fmaf(f, f, acc[t][0]);
+#pragma unroll
+        for (int j = 0; j < kFewExperts; ++j) acc[t][1 + j] = fmaf(f, gw[j][c], acc[t][1 + j]);
       }
     }
   }
 #pragma unroll
   for (int t = 0; t < kDecodeMaxT; ++t) {
     if (t >= Tn) break;
-    const float v = warp_sum(acc[t]);
-    if (lane == 0) logits[(size_t)t * E + e] = bias ? v + bias[e] : v;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float v = warp_sum(acc[t][j]);
+      if (lane == 0) s_part[warp][t * N + j] = v;
+    }
+  }
+  __syncthreads();
+  if (tid < Tn * kFewExperts) {
+    const int t = tid / kFewExperts, j = tid % kFewExperts, e = e0 + j;
+    float ss = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      ss += s_part[w][t * N];
+      l += s_part[w][t * N + 1 + j];
+    }
+    l *= 1.0f / sqrtf(ss / (float)d + eps);
+    if (e < E) logits[(size_t)t * E + e] = bias ? l + bias[e] : l;
   }
 }
-
-bool logits_few_fits(int T, int d) { return T <= kDecodeMaxT && (size_t)T * d * 4 <= 96 * 1024; }
 
 cudaError_t launch_logits_few(ace_dtype dt, const void* u, int T, int d, const float* gamma,
                               float eps, const void* wr, const float* bias, int E, float* logits,
                               uint32_t* status, cudaStream_t s) {
-  const size_t smem = (size_t)T * d * 4;
-  const unsigned grid = (unsigned)cdiv(E, 8);
-  auto go = [&](auto kernel, auto* up, auto* wp) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(kernel, grid, 256, 1, smem, s, up, T, d, gamma, eps, wp, bias, E, logits,
-                             status);
-  };
+  const unsigned grid = (unsigned)cdiv(E, kFewExperts);
   if (dt == ACE_BF16)
-    return go(k_logits_few<__nv_bfloat16>, (const __nv_bfloat16*)u, (const __nv_bfloat16*)wr);
-  return go(k_logits_few<float>, (const float*)u, (const float*)wr);
+    return launch_overlapped(k_logits_few<__nv_bfloat16>, grid, 256, 1, 0, s,
+                             (const __nv_bfloat16*)u, T, d, gamma, eps, (const __nv_bfloat16*)wr,
+                             bias, E, logits, status);
+  return launch_overlapped(k_logits_few<float>, grid, 256, 1, 0, s, (const float*)u, T, d, gamma,
+                           eps, (const float*)wr, bias, E, logits, status);
 }
 
 // logits[i] = the split-K partial sums of element i in split order (+ bias), as
