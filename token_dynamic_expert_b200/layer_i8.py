@@ -15,7 +15,8 @@ One call runs, on the current stream and without a host synchronisation:
 
 The number of kept slots stays on the device: buffers have room for every slot,
 and the kernels stop at the last one in use.  The buffers are allocated once
-(``LayerI8(..., max_tokens)``), so a call can be captured in a CUDA graph.
+(``LayerI8(..., max_tokens)``), so a call can be captured in a CUDA graph; calls of
+one object share them and run one after the other on the device.
 Arithmetic is the operators' (see include/ace.h): integer sums are exact, int8
 rows are correctly rounded, everything else is fp32 with one rounding per stored
 result.
