@@ -451,7 +451,8 @@ ACE_API ace_status ace_tau_quantile(const float* score, int n_tok, int k, int64_
  *     ace_add_rmsnorm -> ace_moe_logits -> ace_gate_topk -> ace_moe_group ->
  *     ace_matmul_i8 (gate and up) -> ace_swiglu -> ace_matmul_i8 (down) ->
  *     ace_moe_combine
- * Every call is asynchronous, allocates nothing and can be captured.  Row
+ * Every call is asynchronous, allocates nothing and can be captured.  Rows,
+ * tokens, slots and E N number at most 2^31 - 256 (ACE_ERR_UNSUPPORTED).  Row
  * strides (ld*) are in elements.  Outputs overlap no input and no other
  * output except where stated; an overlap that the host can see is
  * ACE_ERR_INVALID_ARG.
@@ -553,7 +554,7 @@ ACE_API ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype
  *   all int32 / fp32 device arrays; positions from offsets[E] on are left as
  *   they were.  idx (device) [T][k] int32, keep (device) [T][k] uint8 or
  *   NULL (all kept), gate (device) [T][k] fp32.  An idx outside 0 .. E - 1
- *   counts as skipped.  E <= 512, k <= 16, T k < 2^31.  Deterministic.
+ *   counts as skipped.  E <= 512, k <= 16, Deterministic.
  * ---------------------------------------------------------------------- */
 ACE_API ace_status ace_moe_group(const int32_t* idx, const uint8_t* keep, const float* gate,
                                  int T, int k, int E, int32_t* offsets, int32_t* slot_of,

@@ -168,3 +168,14 @@ def test_logits_refuses(ace):
     assert call(ws_bytes=1024) == ace.ACE_ERR_WORKSPACE
     bad = ace.ace_layer(d=256, E=8, m=64, k=1, dtype=0)
     assert ace.lib().ace_logits_workspace_size(ctypes.byref(bad), 4) == 0
+
+
+def test_counts_near_two_to_the_31(ace):
+    """Rounding such a count up to whole tiles would leave 32 bits."""
+    n = 2 ** 31 - 255
+    assert _norm(ace, T=n) == ace.ACE_ERR_UNSUPPORTED
+    assert _swiglu(ace, S=n) == ace.ACE_ERR_UNSUPPORTED
+    assert _gate(ace, T=n) == ace.ACE_ERR_UNSUPPORTED
+    assert _group(ace, T=n, k=1) == ace.ACE_ERR_UNSUPPORTED
+    assert _matmul(ace, S=n, n_rows=n) == ace.ACE_ERR_UNSUPPORTED
+    assert _matmul(ace, n_rows=n) == ace.ACE_ERR_UNSUPPORTED

@@ -22,6 +22,10 @@ constexpr int kMaxSplitK = 16;
 constexpr int kDecodeMaxT = 8;    // token counts served by the decode kernel
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+// Most rows, tokens or slots of one 8-bit operator: counts rounded up to whole tiles
+// stay in 32 bits.
+constexpr int kMaxCount = 0x7fffff00;
+
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Byte range of `rows` rows of n elements of es bytes, ld elements apart;

@@ -504,7 +504,7 @@ ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype, int T,
                          float* weight, const float* factor, uint8_t* keep, void* stream) {
   if (!opts || (dtype != ACE_BF16 && dtype != ACE_F32)) return ACE_ERR_INVALID_ARG;
   if (T < 0 || E < 1 || k < 1 || k > E || k > kMaxK) return ACE_ERR_INVALID_ARG;
-  if (E > kMaxE) return ACE_ERR_UNSUPPORTED;
+  if (E > kMaxE || T > kMaxCount) return ACE_ERR_UNSUPPORTED;
   if (opts->score != ACE_SCORE_SOFTMAX && opts->score != ACE_SCORE_SIGMOID)
     return ACE_ERR_INVALID_ARG;
   if (opts->group_score != ACE_GROUP_MAX && opts->group_score != ACE_GROUP_TOP2)

@@ -202,7 +202,7 @@ ace_status ace_moe_group(const int32_t* idx, const uint8_t* keep, const float* g
                          int E, int32_t* offsets, int32_t* slot_of, int32_t* slot_token,
                          float* slot_gate, void* stream) {
   if (T < 0 || k < 1 || k > kMaxK || E < 1 || !offsets) return ACE_ERR_INVALID_ARG;
-  if (E > kMaxE || (int64_t)T * k > 0x7fffffff) return ACE_ERR_UNSUPPORTED;
+  if (E > kMaxE || (int64_t)T * k > kMaxCount) return ACE_ERR_UNSUPPORTED;
   if (T > 0 && (!idx || !slot_of || (slot_gate && !gate))) return ACE_ERR_INVALID_ARG;
   if (!is_aligned(idx, 4) || !is_aligned(gate, 4) || !is_aligned(offsets, 4) ||
       !is_aligned(slot_of, 4) || !is_aligned(slot_token, 4) || !is_aligned(slot_gate, 4))

@@ -643,7 +643,8 @@ ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int64_t ldo,
   if (!p || S < 0 || p->N < 1 || p->K < 1 || p->E < 1 || p->n_rows < 0) return ACE_ERR_INVALID_ARG;
   if (out_dtype != ACE_BF16 && out_dtype != ACE_F32) return ACE_ERR_INVALID_ARG;
   if (p->E > kMaxE || p->K % 16 != 0 || p->K > 65536) return ACE_ERR_UNSUPPORTED;
-  if ((int64_t)p->E * p->N > 0x7fffff00) return ACE_ERR_UNSUPPORTED;
+  if ((int64_t)p->E * p->N > kMaxCount || S > kMaxCount || p->n_rows > kMaxCount)
+    return ACE_ERR_UNSUPPORTED;
   if (p->E > 1 && !p->offsets) return ACE_ERR_INVALID_ARG;
   if (!p->row_of && p->n_rows < S) return ACE_ERR_INVALID_ARG;
   if (!ws || !is_aligned(ws, 256) || ws_bytes < 256) return ACE_ERR_WORKSPACE;

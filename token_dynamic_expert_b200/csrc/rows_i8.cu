@@ -458,7 +458,7 @@ ace_status ace_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int
                            float* q_scale, void* stream) {
   if (dtype != ACE_BF16 && dtype != ACE_F32) return ACE_ERR_INVALID_ARG;
   if (T < 0 || d < 1 || !(eps >= 0.f)) return ACE_ERR_INVALID_ARG;
-  if (d > kMaxRow) return ACE_ERR_UNSUPPORTED;
+  if (d > kMaxRow || T > kMaxCount) return ACE_ERR_UNSUPPORTED;
   if (T == 0) return ACE_OK;
   if ((!sum && !y && !q) || (q && !q_scale)) return ACE_ERR_INVALID_ARG;
   const size_t es = dtype == ACE_BF16 ? 2 : 4;
@@ -490,7 +490,7 @@ ace_status ace_swiglu(const void* gu, int64_t ldgu, int S, int m, ace_dtype dtyp
                       float* q_scale, void* stream) {
   if (dtype != ACE_BF16 && dtype != ACE_F32) return ACE_ERR_INVALID_ARG;
   if (S < 0 || m < 1) return ACE_ERR_INVALID_ARG;
-  if (m > kMaxRow) return ACE_ERR_UNSUPPORTED;
+  if (m > kMaxRow || S > kMaxCount) return ACE_ERR_UNSUPPORTED;
   if (S == 0) return ACE_OK;
   if ((!y && !q) || (q && !q_scale)) return ACE_ERR_INVALID_ARG;
   const size_t es = dtype == ACE_BF16 ? 2 : 4;
