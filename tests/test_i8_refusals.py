@@ -179,3 +179,14 @@ def test_counts_near_two_to_the_31(ace):
     assert _group(ace, T=n, k=1) == ace.ACE_ERR_UNSUPPORTED
     assert _matmul(ace, S=n, n_rows=n) == ace.ACE_ERR_UNSUPPORTED
     assert _matmul(ace, n_rows=n) == ace.ACE_ERR_UNSUPPORTED
+
+
+def test_router_layer_refuses(ace):
+    """What the kernels would read past the end of."""
+    g, w, b = torch.ones(64), torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(8)
+    assert ace.make_router_layer(g, w, b).E == 8
+    for bad, err in (((g.bfloat16(), w), TypeError), ((g[:32], w), ValueError), ((g, w[0]), ValueError),
+                     ((g, w.half()), TypeError), ((g, w[:, ::2]), ValueError), ((g, w, b[:7]), ValueError),
+                     ((g, w, b.double()), TypeError), ((g, w[:, :32], b), ValueError)):
+        with pytest.raises(err):
+            ace.make_router_layer(*bad)

@@ -379,13 +379,17 @@ def ace_add_rmsnorm(x, gamma, residual=None, sum=None, y=None, q=None, q_scale=N
 
 def make_router_layer(gamma, w_router, router_bias=None):
     """An ``ace_layer`` holding only gamma and the router (for
-    ace_moe_logits): E, d from w_router [E][d]."""
-    for t in (gamma, w_router, router_bias):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+    ace_moe_logits): E, d from w_router [E][d]; gamma [d] and router_bias [E]
+    fp32 on the same device.  The caller keeps the tensors alive while the
+    struct is in use."""
+    if w_router.dim() != 2:
+        raise ValueError("w_router must be [E][d]")
     E, d = w_router.shape
-    return ace_layer(d=d, E=E, m=64, k=1, dtype=_dtype_code(w_router), gamma=_ptr(gamma),
-                     w_router=_ptr(w_router), router_bias=_ptr(router_bias))
+    dev = w_router.get_device()
+    return ace_layer(d=d, E=E, m=64, k=1, dtype=_dtype_code(w_router),
+                     gamma=_arg(gamma, "gamma", dev, torch.float32, (d,)),
+                     w_router=_arg(w_router, "w_router", dev, w_router.dtype, (E, d)),
+                     router_bias=_arg(router_bias, "router_bias", dev, torch.float32, (E,)))
 
 
 def ace_logits_workspace_size(layer, max_tokens):
