@@ -227,3 +227,24 @@ def test_refusals():
                          L.s_down, 2, 8)
     with pytest.raises(ValueError, match="match"):
         layer_i8.LayerI8(L.gamma, L.w_router[:4], L.wq_gu, L.s_gu, L.wq_down, L.s_down, 2, 8)
+
+
+def test_rows_that_lie_apart():
+    """Rows of u and residual within wider ones give the bits of contiguous rows;
+    a y or sum of that kind is refused, and its neighbours stay as they were."""
+    L, u, res = _make(24, 256, 8, 64, 2)
+    wide = torch.randn(24, 768, device="cuda").bfloat16()
+    wide[:, :256], wide[:, 256:512] = u, res
+    for r, rw in ((None, None), (res, wide[:, 256:512])):
+        want, got = torch.empty_like(u), torch.empty_like(u)
+        L.forward(u, want, r)
+        L.forward(wide[:, :256], got, rw)
+        assert torch.equal(want, got) and L.status()[0] == 0
+    before = wide.clone()
+    with pytest.raises(ValueError, match="contiguous"):
+        L.forward(u, wide[:, 512:])
+    with pytest.raises(ValueError, match="contiguous"):
+        L.forward(u, torch.empty_like(u), res, sum=wide[:, 512:])
+    with pytest.raises(ValueError, match="device"):
+        L.forward(u, torch.empty(24, 256, dtype=u.dtype))
+    assert torch.equal(wide, before)

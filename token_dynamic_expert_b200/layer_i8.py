@@ -81,12 +81,15 @@ class LayerI8:
     def forward(self, u, y, residual=None, sum=None, tau=0.0, stream=None):
         """y [T][d] = the layer's output for u [T][d] (+ residual; sum, if given,
         receives u + residual, and may be either of them).  Slots but a token's
-        largest are skipped where weight * factor < tau.  T <= max_tokens."""
+        largest are skipped where weight * factor < tau.  T <= max_tokens.  Rows of
+        u and residual may lie apart; y and sum are contiguous."""
         T, k, E = u.shape[0], self.k, self.E
         if T > self.max_tokens or u.shape[1] != self.d or u.dtype != self.dtype:
             raise ValueError("u must be [T <= %d][%d] %s" % (self.max_tokens, self.d, self.dtype))
-        if y.shape != u.shape or y.dtype != u.dtype:
-            raise ValueError("y must have u's shape and dtype")
+        if y.shape != u.shape or y.dtype != u.dtype or y.get_device() != u.get_device():
+            raise ValueError("y must have u's shape, dtype and device")
+        if not y.is_contiguous() or (sum is not None and not sum.is_contiguous()):
+            raise ValueError("y and sum must be contiguous")
         if T == 0:
             return y
         if stream is not None:
@@ -97,8 +100,8 @@ class LayerI8:
                 return self.forward(u, y, residual, sum, tau)
         S = T * k
         xq, xs, logits = self.xq[:T], self.xs[:T], self.logits[:T]
-        if residual is not None and sum is None:
-            sum = self.sum[:T]
+        if sum is None and (residual is not None or not u.is_contiguous()):
+            sum = self.sum[:T]  # the router reads whole rows
         idx, weight, keep = (t[:S].view(T, k) for t in (self.idx, self.weight, self.keep))
         slot_of, slot_token, slot_gate = self.slot_of[:S].view(T, k), self.slot_token[:S], self.slot_gate[:S]
         gu, hq, hs, yslot = self.gu[:S], self.hq[:S], self.hs[:S], self.yslot[:S]
