@@ -94,10 +94,17 @@ __device__ __forceinline__ void group_top2(F& a, F& b, int lg) {
   }
 }
 
-// fkey for doubles (neither NaN nor -0: the callers add +0 and keep NaN out).
+// gate_key for doubles.
 __device__ __forceinline__ unsigned long long dkey(double v) {
   const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
-  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+  return v != v ? ~0ull : (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+
+// A softmax score from t = e^(x - m) and the sum z.  NaN stays with the experts that
+// cause it (a NaN logit, +infinity less the maximum); it makes z NaN, and the
+// token's other scores count as 0.
+__device__ __forceinline__ double share64(double t, double z) {
+  return t != t ? t : z > 0.0 ? t / z : 0.0;
 }
 
 // Largest 64-bit value over the warp, by its halves.
@@ -137,7 +144,7 @@ __device__ __noinline__ int choose64(const GateArgs& A, const TL* row, int lane,
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (!A.sigmoid) c[j] = z > 0.0 ? c[j] / z : 0.0;
+      if (!A.sigmoid) c[j] = share64(c[j], z);
       if (A.bias && j < L.n) c[j] += (double)A.bias[L.e0 + j];
     }
   }
@@ -205,15 +212,14 @@ __device__ __noinline__ int order64(const GateArgs& A, const TL* row, const Lane
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   }
   const bool on = lane <= A.k && e >= 0;
-  double c = -INFINITY;
+  unsigned long long c = 0ull;
   if (on) {
     const double x = (double)logit_at(row, e);
-    c = A.sigmoid ? 1.0 / (1.0 + exp(-x)) : z > 0.0 ? exp(x - m) / z : 0.0;
-    c += (double)A.bias[e];
+    c = dkey((A.sigmoid ? 1.0 / (1.0 + exp(-x)) : share64(exp(x - m), z)) + (double)A.bias[e]);
   }
-  int rank = 0;
+  int rank = 0;  // a place of its own for every expert: keys order NaN too
   for (int j = 0; j <= A.k; ++j) {
-    const double o = __shfl_sync(0xffffffffu, c, j);
+    const unsigned long long o = __shfl_sync(0xffffffffu, c, j);
     const int oe = __shfl_sync(0xffffffffu, e, j);
     rank += oe >= 0 && (o > c || (o == c && oe < e));
   }
