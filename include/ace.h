@@ -511,7 +511,7 @@ typedef struct {
                                   1 <= n_groups <= 32, dividing E          */
   int topk_groups;             /* groups whose experts may be chosen       */
   ace_group_score group_score; /* the group's largest choice value, or the
-                                  sum of its two largest                   */
+                                  sum of its two largest (of one: its own) */
   int renorm_topk;             /* 1: weights divided by the chosen scores'
                                   sum; 0: the scores themselves            */
   float scale;                 /* factor on every weight, > 0              */
@@ -538,7 +538,7 @@ typedef struct {
  *   A logit of -infinity is an expert out of service: score 0 (it is chosen
  *   only when nothing better is left, or by its bias).  A token whose
  *   chosen scores sum to 0 gets weights 0.  NaN compares above +infinity and
- *   makes the token's weights NaN.
+ *   makes the token's weights NaN.  idx names k different experts in every case.
  * ---------------------------------------------------------------------- */
 ACE_API ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype, int T, int E,
                                  int k, const float* bias, const ace_gate_opts* opts, int32_t* idx,

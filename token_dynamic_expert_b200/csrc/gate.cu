@@ -82,22 +82,26 @@ __device__ __forceinline__ uint32_t gate_key(float v) {
   return v == v ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0xffffffffu;
 }
 
-// Largest two of the values held by the lg neighbouring lanes of a group.
-template <typename F>
-__device__ __forceinline__ void group_top2(F& a, F& b, int lg) {
+// Largest two of the keys held by the lg neighbouring lanes of a group (a >= b in
+// each lane).  Keys are integers, so every lane of the group ends with the same two,
+// whatever the values were; floats compared by > would leave a NaN with its own lane.
+template <typename U>
+__device__ __forceinline__ void group_top2(U& a, U& b, int lg) {
   for (int o = 1; o < lg; o <<= 1) {
-    const F oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-    const F second = oa > a ? a : oa;
-    a = oa > a ? oa : a;
-    b = b > ob ? b : ob;
-    b = second > b ? second : b;
+    const U oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+    b = max(max(b, ob), min(a, oa));
+    a = max(a, oa);
   }
 }
 
-// gate_key for doubles.
+// gate_key for doubles, and the double of a key.
 __device__ __forceinline__ unsigned long long dkey(double v) {
   const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
   return v != v ? ~0ull : (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double dkey_inv(unsigned long long k) {
+  return __longlong_as_double(
+      (long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
 
 // A softmax score from t = e^(x - m) and the sum z.  NaN stays with the experts that
@@ -150,15 +154,15 @@ __device__ __noinline__ int choose64(const GateArgs& A, const TL* row, int lane,
   }
   bool allowed = true;
   if (A.G > 1) {
-    double a = -INFINITY, b = -INFINITY;
+    unsigned long long a = 0ull, b = 0ull;  // below every key
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const double v = j < L.n ? c[j] : -INFINITY;
-      b = v > a ? a : (v > b ? v : b);
-      a = v > a ? v : a;
+      const unsigned long long v = j < L.n ? dkey(c[j]) : 0ull;
+      b = max(b, min(a, v));
+      a = max(a, v);
     }
     group_top2(a, b, lg);
-    const unsigned long long gv = dkey(A.top2 ? a + b : a);
+    const unsigned long long gv = A.top2 ? dkey(dkey_inv(a) + dkey_inv(b)) : a;
     int rank = 0;
     for (int h = 0; h < A.G; ++h) {
       const unsigned long long o = __shfl_sync(0xffffffffu, gv, h * lg);
@@ -347,24 +351,19 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
   bool near = false;
 
   if (A.G > 1) {
-    float a = -INFINITY, b = -INFINITY;
-    if (c[0] != 0ull) a = fkey_inv((uint32_t)(c[0] >> 32));
-    if (NV > 1 && c[NV > 1 ? 1 : 0] != 0ull) b = fkey_inv((uint32_t)(c[NV > 1 ? 1 : 0] >> 32));
-    float gv;
-    if (A.top2) {
-      if (!BIAS) {  // the keys are logits
-        a = c[0] != 0ull ? about(a) : a;
-        b = (NV > 1 && c[NV > 1 ? 1 : 0] != 0ull) ? about(b) : -INFINITY;
-      }
-      group_top2(a, b, lg);
-      gv = a + b;
-    } else {
-      group_top2(a, b, lg);
-      gv = a;
-      b = 0.f;
+    uint32_t a = (uint32_t)(c[0] >> 32), b = NV > 1 ? (uint32_t)(c[NV > 1 ? 1 : 0] >> 32) : 0u;
+    if (!BIAS && A.top2) {  // the keys are logits
+      a = a != 0u ? gate_key(about(fkey_inv(a))) : 0u;
+      b = b != 0u ? gate_key(about(fkey_inv(b))) : 0u;
     }
-    const float mag = fabsf(a) + fabsf(b);
-    const uint32_t gk = L.group < A.G ? gate_key(gv) : 0u;
+    group_top2(a, b, lg);
+    uint32_t gk = a;  // a group's lanes agree on it; 0 beyond the last group
+    float mag = fabsf(fkey_inv(a));
+    if (A.top2) {  // then a group has two experts at least
+      mag += fabsf(fkey_inv(b));
+      gk = a != 0u ? gate_key(fkey_inv(a) + fkey_inv(b)) : 0u;
+    }
+    mag = mag == mag ? mag : 0.f;  // a NaN group is above all others, whatever they are
     int rank = 0;
     for (int h = 0; h < A.G; ++h) {
       const uint32_t o = __shfl_sync(0xffffffffu, gk, h * lg);
@@ -377,7 +376,9 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
       const uint32_t next = __reduce_max_sync(0xffffffffu, !allowed && L.group < A.G ? gk : 0u);
       const float top = __uint_as_float(
           __reduce_max_sync(0xffffffffu, L.group < A.G ? __float_as_uint(mag) : 0u));
-      near = next != 0u && fkey_inv(last) - fkey_inv(next) <= 2.f * (2.f * err + 1.5e-7f * top);
+      // (a difference of two infinities, fp32 sums that overflowed, counts as near)
+      near = next != 0u &&
+             !(fkey_inv(last) - fkey_inv(next) > 2.f * (2.f * err + 1.5e-7f * top));
     }
     if (!allowed) c[0] = 0ull;
   }
@@ -434,6 +435,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
 
   // weights
   const bool on = lane < A.k;
+  my_e = max(my_e, 0);  // lanes behind the experts that were found
   if (on) my_x = logit_at(row, my_e);
   float w = 0.f;
   if (A.renorm) {
