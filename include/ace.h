@@ -537,8 +537,10 @@ typedef struct {
  *   most the experts of topk_groups groups.
  *   A logit of -infinity is an expert out of service: score 0 (it is chosen
  *   only when nothing better is left, or by its bias).  A token whose
- *   chosen scores sum to 0 gets weights 0.  NaN compares above +infinity and
- *   makes the token's weights NaN.  idx names k different experts in every case.
+ *   chosen scores sum to 0 gets weights 0.  NaN compares above +infinity.  A
+ *   NaN logit, of any expert, makes all the token's weights NaN, and so does
+ *   +infinity with softmax: such an expert's score is NaN, the token's other
+ *   softmax scores count as 0.  idx names k different experts in every case.
  * ---------------------------------------------------------------------- */
 ACE_API ace_status ace_gate_topk(const void* logits, int64_t ld, ace_dtype dtype, int T, int E,
                                  int k, const float* bias, const ace_gate_opts* opts, int32_t* idx,

@@ -1,6 +1,7 @@
 """ace_gate_topk on tokens that hold NaN or infinite logits and biases: the
-experts are those of a sort in 64 bits in which NaN stands above +infinity, and none
-is named twice."""
+experts are those of a sort in 64 bits in which NaN stands above +infinity, none is
+named twice, and a NaN logit (with softmax a +infinity too) makes the token's
+weights NaN."""
 import itertools
 
 import numpy as np
@@ -61,9 +62,18 @@ def _check(x, k, bias=None, score="softmax", G=1, tg=1, rule="max", renorm=True,
     factor = torch.rand(E, device="cuda") + 0.5
     ace.ace_gate_topk(x, idx, w, bias=bias, score=score, n_groups=G, topk_groups=tg, group_score=rule,
                       renorm=renorm, scale=scale, factor=factor, tau=0.05, keep=keep)
-    got = idx.cpu().numpy()
-    ri, _ = _gate(ora.f64(x), k, None if bias is None else ora.f64(bias), score, G, tg, rule, renorm, scale)
+    got, gw = idx.cpu().numpy(), w.cpu().double().numpy()
+    ri, rw = _gate(ora.f64(x), k, None if bias is None else ora.f64(bias), score, G, tg, rule, renorm, scale)
     assert np.array_equal(got, ri)
+    assert np.array_equal(np.isnan(gw), np.isnan(rw))
+    v = ora.f64(x)
+    v = v[np.isfinite(v)]
+    ok = ~np.isnan(rw)  # the bound of the finite tokens' tests
+    assert ora.close(gw[ok], rw[ok], (2 * (v.max() - v.min()) + 20) * ora.U32, 1e-37) <= 1
+    # the skip rule: NaN is not below tau, and the largest of the others is kept
+    want = ~(w * factor[idx.long()] < 0.05).cpu().numpy()
+    want[np.arange(T), np.where(np.isnan(gw), INF, gw).argmax(1)] = True  # numpy: the first of equals
+    assert np.array_equal(keep.cpu().numpy() != 0, want)
 
 
 def _tokens(E, G, value, dt, seed):

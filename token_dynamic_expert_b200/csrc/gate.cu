@@ -337,6 +337,17 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
           }
         }
 
+  // A NaN logit, or +infinity under softmax, leaves the token's weights undefined.
+  // A lane's first key shows whether to look (a NaN may come from the bias alone).
+  bool undefined = false;
+  if (__any_sync(0xffffffffu, (uint32_t)(c[0] >> 32) >= (SIG || BIAS ? 0xffffffffu : 0xff800000u))) {
+    for (int j = 0; j < L.n; ++j) {
+      const float v = logit_at(row, L.e0 + j);
+      undefined |= v != v || (!SIG && v == INFINITY);
+    }
+    undefined = __any_sync(0xffffffffu, undefined);
+  }
+
   // Bound on the fp32 error of a score that decides, u = 2^-24:
   //   sigmoid: e^-x has the relative error of its argument's rounding and of
   //   log2 e, 1.22 |x| u, and of ex2.approx, 4 u; s moves by s (1 - s) of that, at
@@ -441,7 +452,6 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
   if (A.renorm) {
     // relative to the largest chosen logit, so that no sum underflows
     float top = on ? my_x : -INFINITY;
-    const bool nan = __any_sync(0xffffffffu, on && my_x != my_x);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (top != -INFINITY && on) {
@@ -455,11 +465,11 @@ __global__ void __launch_bounds__(kGateWarps * 32) k_gate_topk(const GateArgs A)
     float sum = w;  // the k <= 16 chosen lie on the first 16 lanes
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    w = nan ? __uint_as_float(0x7fffffffu) : (sum > 0.f ? w / sum : (sum != sum ? sum : 0.f));
+    w = sum > 0.f ? w / sum : 0.f;
   } else if (on) {
     w = score(my_x);
   }
-  w *= A.scale;
+  w = undefined ? __uint_as_float(0x7fffffffu) : w * A.scale;
   if (on) {
     const size_t o = (size_t)t * A.k + lane;
     A.idx[o] = my_e;
