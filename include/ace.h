@@ -467,8 +467,8 @@ ACE_API ace_status ace_tau_quantile(const float* score, int n_tok, int k, int64_
  *     M_t = max_j |s_tj gamma_j|,  q_tj = nearest int of 127 s_tj gamma_j / M_t
  *     q_scale_t = M_t r_t / 127
  *   so q q_scale stands for s r gamma before its rounding.  q is the correctly
- *   rounded quotient (halves to even), |q| <= 127.  Sums are fp32; s and y are
- *   rounded once to dtype.
+ *   rounded quotient (halves to even), |q| <= 127.  Sums are fp32, a sum of
+ *   squares beyond fp32's range fp64; s and y are rounded once to dtype.
  *   x, residual, sum, y (device) [T][d] dtype, aligned to their element;
  *   residual, sum, y and q may each be NULL (one output at least); gamma
  *   (device) [d] fp32; q (device) [T][d] int8 with q_scale (device) [T] fp32.
@@ -476,8 +476,8 @@ ACE_API ace_status ace_tau_quantile(const float* score, int n_tok, int k, int64_
  *   1 <= d <= 16384 (ACE_ERR_UNSUPPORTED above), any T >= 0, eps >= 0.  Rows
  *   that start on 16-byte boundaries and a d that is a multiple of 16 bytes
  *   move in 16-byte vectors; every other case is served, more slowly.
- *   A row whose sum of squares or M is not finite in fp32 gets q = 0 and
- *   q_scale = NaN; a row with M < 2^-126 gets q = 0 and q_scale = 0.
+ *   A row whose M is not finite in fp32 gets q = 0 and q_scale = NaN; a row
+ *   with M < 2^-126 gets q = 0 and q_scale = 0.
  * ---------------------------------------------------------------------- */
 ACE_API ace_status ace_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                    int T, int d, ace_dtype dtype, const float* gamma, float eps,

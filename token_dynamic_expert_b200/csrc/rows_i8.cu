@@ -31,8 +31,16 @@ namespace {
 
 constexpr int kRowWarps = 4;          // rows of a CTA, where a warp holds one
 constexpr int kMaxRow = 16384;        // elements per row
+constexpr float kMinMax = 1.17549435e-38f;  // 2^-126: below it q = 0
 constexpr float kTinyMax = 7.9e-31f;  // 2^-100: below it 127 / M may overflow
 constexpr float kHugeMax = 8.5e37f;   // 2^126: above it the fast quotient is 0
+
+// A sum of squares that fp32 does not hold.  Above kHugeSum it has overflowed.  Below
+// kTinySum the squares of elements under 2^-63 have lost bits: 16384 roundings of
+// 2^-150 at most, 2^-36 of kTinySum, and nothing to an eps from kSmallEps on.
+constexpr float kHugeSum = 3.4e38f;
+constexpr float kTinySum = 7.9e-31f;   // 2^-100
+constexpr float kSmallEps = 8.1e-28f;  // 2^-90
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -218,9 +226,55 @@ __device__ __forceinline__ void load_gamma(const float* gamma, int at, float (&g
   }
 }
 
+// y and q_scale of a row (norm) whose sum of squares fp32 does not hold: sum and r in
+// fp64, which holds the squares of fp32 values of any size.  q_scale comes with M in it.
+// s is read again (each thread its own elements, so y may be in place): a call at the
+// kernel's end with nothing but its arguments alive leaves the kernel its registers.
+// Forms that kept s or M for it took 8 more, a block less on an SM (4000 rows of 4096:
+// 26.5 us without any of this, 28.6 with those, 26.8 with this).
+template <typename T, int V, bool ONE>
+__device__ __noinline__ void far_row(const RowArgs& A) {
+  __shared__ double s_sum[32];
+  const int lane = threadIdx.x & 31, tid = ONE ? lane : threadIdx.x;
+  const int64_t row =
+      ONE ? (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  const int step = ONE ? 32 : blockDim.x;
+  const T* x = static_cast<const T*>(A.sum ? A.sum : A.a) + row * (A.sum ? A.lds : A.lda);
+  const T* b = A.sum || !A.b ? nullptr : static_cast<const T*>(A.b) + row * A.ldb;
+  auto s_at = [&](int j) { return b ? to_f(from_f<T>(to_f(x[j]) + to_f(b[j]))) : to_f(x[j]); };
+  double sum = 0.0;
+#pragma unroll 1
+  for (int at = tid * V; at < A.d; at += step * V)
+#pragma unroll 1
+    for (int j = at; j < at + V; ++j) sum += (double)s_at(j) * (double)s_at(j);
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (!ONE) {
+    if (lane == 0) s_sum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll 1
+    for (int w = 0; w < step / 32; ++w) sum += s_sum[w];
+  }
+  const double r = 1.0 / sqrt(sum / A.d + (double)A.eps);
+  if (A.y != nullptr)
+#pragma unroll 1
+    for (int at = tid * V; at < A.d; at += step * V)
+#pragma unroll 1
+      for (int j = at; j < at + V; ++j)
+        static_cast<T*>(A.y)[row * A.ldy + j] =
+            from_f<T>(__fmul_rn((float)((double)s_at(j) * r), A.gamma[j]));
+  if (A.q != nullptr && tid == 0) {
+    const float M = A.q_scale[row];  // 0 and NaN stay
+    if (M > 0.f) A.q_scale[row] = (float)((double)M * r / 127.0);
+  }
+}
+
 // ONE: a warp a row and kRowWarps rows a CTA, no barrier; else a CTA a row.
+// far_args: A once more, for far_row, which takes its address (with A's own address
+// taken the norm of 21845 rows of 768 took 36.7 us instead of 30.5).
 template <typename T, int V, int ITEMS, bool SWIGLU, bool ONE>
-__global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1) k_rows_i8(const RowArgs A) {
+__global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1)
+    k_rows_i8(const RowArgs A, const __grid_constant__ RowArgs far_args) {
   constexpr float kRel = rel_bound<SWIGLU>();
   __shared__ float s_ss[32];
   __shared__ uint32_t s_mx[32];
@@ -297,8 +351,9 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1) k_rows_i8(cons
   }
   const float r = SWIGLU ? 1.f : 1.0f / sqrtf(ss / (float)d + A.eps);
   const float M = __uint_as_float(mb);
-  const bool finite = isfinite(M) && (SWIGLU || isfinite(ss));
-  const bool usable = finite && M >= 1.17549435e-38f;  // else no element to scale by: q = 0
+  const bool finite = isfinite(M);  // an element that is not makes M so
+  const bool far_ss = !SWIGLU && (ss > kHugeSum || (ss < kTinySum && A.eps < kSmallEps));
+  const bool usable = finite && M >= kMinMax;  // else no element to scale by: q = 0
   const bool far = M < kTinyMax || M > kHugeMax;  // 127 / M in fp32 is no use: fp64 decides all
   // (the exact division costs SwiGLU 1 us of 36 at 65536 rows of 512)
   const float inv = !usable || far ? 0.f : SWIGLU ? quotient(127.f, M) : __fdiv_rn(127.f, M);
@@ -311,7 +366,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1) k_rows_i8(cons
     if (at >= nv) continue;
     float g[V];
     if (!SWIGLU) load_gamma<V>(A.gamma, at, g);
-    if (A.y != nullptr) {
+    if (A.y != nullptr && !far_ss) {
       float o[V];
 #pragma unroll
       for (int c = 0; c < V; ++c) o[c] = SWIGLU ? v[i][c] : xhat(v[i][c], r, g[c]);
@@ -331,44 +386,45 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1) k_rows_i8(cons
       reinterpret_cast<Vec<int8_t, V>*>(A.q + row * A.ldq)[at] = low_bytes<V>(o);
     }
   }
-  if (A.q == nullptr) return;
-  if (tid == 0)
-    A.q_scale[row] = usable ? M * (r * (1.f / 127.f)) : finite ? 0.f : __uint_as_float(0x7fc00000u);
-  if (ONE ? !__any_sync(0xffffffffu, differ != 0u) : !__syncthreads_or((int)differ)) return;
-
-  // fp64: first M, from the elements that fp32 cannot tell from the largest
-  if (ONE) __syncwarp();  // s_top is 0 for every lane
-  const float cand = M * (1.f - 4.f * kRel);
+  if (A.q != nullptr && tid == 0)
+    A.q_scale[row] = usable ? (far_ss ? M : M * (r * (1.f / 127.f))) : finite ? 0.f : __uint_as_float(0x7fc00000u);
+  if (A.q != nullptr && (ONE ? __any_sync(0xffffffffu, differ != 0u) : __syncthreads_or((int)differ) != 0)) {
+    // fp64: first M, from the elements that fp32 cannot tell from the largest
+    if (ONE) __syncwarp();  // s_top is 0 for every lane
+    const float cand = M * (1.f - 4.f * kRel);
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int at = i * nt + tid;
-    if (at >= nv) continue;
+    for (int i = 0; i < ITEMS; ++i) {
+      const int at = i * nt + tid;
+      if (at >= nv) continue;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float p = SWIGLU ? v[i][c] : v[i][c] * A.gamma[at * V + c];
-      if (fabsf(p) >= cand)
-        atomicMax(&s_top, (unsigned long long)__double_as_longlong(
-                              fabs(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU))));
+      for (int c = 0; c < V; ++c) {
+        const float p = SWIGLU ? v[i][c] : v[i][c] * A.gamma[at * V + c];
+        if (fabsf(p) >= cand)
+          atomicMax(&s_top, (unsigned long long)__double_as_longlong(
+                                fabs(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU))));
+      }
+    }
+    if (ONE)
+      __syncwarp();
+    else
+      __syncthreads();
+    const double top = __longlong_as_double((long long)s_top);
+    if (differ != 0u) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int at = i * nt + tid;
+        if (at >= nv) continue;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float p = SWIGLU ? v[i][c] : v[i][c] * A.gamma[at * V + c];
+          if (far || fmaf(p, inv_lo, kMagic) != fmaf(p, inv_hi, kMagic))
+            A.q[row * A.ldq + at * V + c] =
+                (int8_t)quotient64(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU), top);
+        }
+      }
     }
   }
-  if (ONE)
-    __syncwarp();
-  else
-    __syncthreads();
-  const double top = __longlong_as_double((long long)s_top);
-  if (differ == 0u) return;
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int at = i * nt + tid;
-    if (at >= nv) continue;
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float p = SWIGLU ? v[i][c] : v[i][c] * A.gamma[at * V + c];
-      if (far || fmaf(p, inv_lo, kMagic) != fmaf(p, inv_hi, kMagic))
-        A.q[row * A.ldq + at * V + c] =
-            (int8_t)quotient64(exact_p(a, A.gamma, v[i][c], d, at * V + c, SWIGLU), top);
-    }
-  }
+  if (far_ss) far_row<T, V, ONE>(far_args);  // the same for the whole row
 }
 
 template <typename T, int V, int ITEMS, bool SWIGLU>
@@ -378,15 +434,15 @@ cudaError_t launch_cta(const RowArgs& A, cudaStream_t s) {
   // Few rows may start while the kernel before ends (3.0 -> 2.7 us for 61 rows of
   // SwiGLU).  With many, a wait in each of the small CTAs costs more than the
   // launch (65536 rows: 51 -> 81 us).
-  if (A.overlap) return launch_overlapped(kernel, (unsigned)A.rows, threads, 1, 0, s, A);
-  kernel<<<(unsigned)A.rows, threads, 0, s>>>(A);
+  if (A.overlap) return launch_overlapped(kernel, (unsigned)A.rows, threads, 1, 0, s, A, A);
+  kernel<<<(unsigned)A.rows, threads, 0, s>>>(A, A);
   return cudaGetLastError();
 }
 
 template <typename T, int V, int ITEMS, bool SWIGLU>
 cudaError_t launch_warp(const RowArgs& A, cudaStream_t s) {
   k_rows_i8<T, V, ITEMS, SWIGLU, true>
-      <<<(unsigned)cdiv(A.rows, kRowWarps), 32 * kRowWarps, 0, s>>>(A);
+      <<<(unsigned)cdiv(A.rows, kRowWarps), 32 * kRowWarps, 0, s>>>(A, A);
   return cudaGetLastError();
 }
 
