@@ -602,8 +602,8 @@ ACE_API ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int6
  *     h_j = g_j / (1 + exp(-g_j)) u_j,  M = max_j |h_j|,
  *     q_j = nearest int of 127 h_j / M,  q_scale = M / 127
  *   q as in ace_add_rmsnorm (correctly rounded; rows that are not finite and
- *   rows of zeros likewise); y = h rounded to dtype.  Where g is below
- *   -126 ln 2 = -87.3, exp(-g) leaves fp32 and h counts as 0.
+ *   rows of zeros likewise); y = h rounded to dtype.  A g of -infinity counts
+ *   as SiLU's limit, 0; a row with a g below -87 is formed in fp64.
  *   gu (device) [S][2 m] dtype; y (device) [S][m] dtype or NULL; q (device)
  *   [S][m] int8 or NULL, with q_scale (device) [S] fp32 (y or q is given).
  *   n_valid (device, one int32) or NULL: rows from *n_valid on are not read

@@ -74,3 +74,75 @@ def test_norm_of_zero_rows_without_eps():
     x = torch.zeros(3, 256, device="cuda")
     o = _norm(x, torch.ones(256, device="cuda"), 0.0)
     assert o["y"].isnan().all() and (o["q"] == 0).all() and (o["q_scale"] == 0).all()
+
+
+def _swiglu(gu, dt):
+    from token_dynamic_expert_b200 import ace
+    S, m = gu.shape[0], gu.shape[1] // 2
+    o = dict(y=torch.full((S, m), 7, dtype=gu.dtype, device="cuda"),
+             q=torch.full((S, m), 99, dtype=torch.int8, device="cuda"), q_scale=torch.full((S,), 7.0, device="cuda"))
+    ace.ace_swiglu(gu, **o)
+    torch.cuda.synchronize()
+    return o
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("S,m", [(3, 64), (5, 768), (700, 512), (700, 2048), (2, 16384), (3, 1001)])
+def test_swiglu_of_gates_far_below_zero(dt, S, m):
+    """g from -100 to -80: SiLU(g) falls from 1e-33 to 4e-42, g e^g, past where its
+    reciprocal leaves fp32 (-87.3); rows of them alone, and of one beside ordinary ones."""
+    g = torch.Generator(device="cuda").manual_seed(S + m)
+    gu = torch.randn(S, 2 * m, generator=g, device="cuda") * 2
+    gu[:, :m] = torch.linspace(-100, -80, m, device="cuda")
+    gu[:, m:] *= 2.0 ** torch.randint(-8, 60, (S, 1), generator=g, device="cuda")
+    gu[1] = torch.randn(2 * m, generator=g, device="cuda")
+    gu[1, m // 2] = -90.0
+    gu = gu.to(DT[dt])
+    o = _swiglu(gu, dt)
+    h, q, scale = ora.swiglu(ora.f64(gu))
+    # h in fp32 (half a step below the normal numbers), then y's rounding
+    assert ora.close(ora.f64(o["y"]), h, ora.HALF[dt] + 11 * ora.U32, 2 * STEP[dt]) <= 1
+    used = np.abs(h).max(1) >= 2.0 ** -126
+    assert used.sum() >= min(S, 3) - 1 and used[1]
+    assert np.array_equal(o["q"].cpu().numpy()[used], q[used])
+    assert ora.close(ora.f64(o["q_scale"])[used], scale[used], 13 * ora.U32) <= 1
+    assert not o["q"].cpu().numpy()[~used].any() and not o["q_scale"].cpu().numpy()[~used].any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("S,m", [(2, 64), (700, 512), (3, 1001)])
+def test_swiglu_of_gates_at_minus_infinity(dt, S, m):
+    """SiLU's limit, 0: a channel that is masked out so leaves its row's others alone."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    gu = torch.randn(S, 2 * m, generator=g, device="cuda").to(DT[dt])
+    masked = torch.rand(S, m, generator=g, device="cuda") < 0.3
+    zeros = gu.clone()
+    gu[:, :m][masked] = -float("inf")
+    zeros[:, :m][masked] = 0.0
+    # the row of zeros in 64 bits: such a row is formed by another path than one without
+    # them, so y and scale agree within their tolerance, not bit for bit
+    o = _swiglu(gu, dt)
+    h, q, scale = ora.swiglu(ora.f64(zeros))
+    assert ora.close(ora.f64(o["y"]), h, ora.HALF[dt] + 11 * ora.U32, 2 * STEP[dt]) <= 1
+    assert np.array_equal(o["q"].cpu().numpy(), q) and (o["y"][masked] == 0).all()
+    assert ora.close(ora.f64(o["q_scale"]), scale, 13 * ora.U32) <= 1
+
+
+def test_swiglu_low_gates_in_each_output_alone_and_with_nan():
+    from token_dynamic_expert_b200 import ace
+    for S, m in ((4, 96), (700, 96), (700, 2048)):
+        gu = torch.randn(S, 2 * m, device="cuda")
+        gu[:, 3] = -88.0
+        gu[1, 5], gu[2, m + 3] = float("nan"), float("inf")
+        both = _swiglu(gu, "f32")
+        y = torch.empty(S, m, device="cuda")
+        q, qs = torch.empty(S, m, dtype=torch.int8, device="cuda"), torch.empty(S, device="cuda")
+        ace.ace_swiglu(gu, y=y)
+        ace.ace_swiglu(gu, q=q, q_scale=qs)
+        assert torch.equal(y.view(torch.int32), both["y"].view(torch.int32))
+        assert torch.equal(q, both["q"]) and torch.equal(qs.view(torch.int32), both["q_scale"].view(torch.int32))
+        assert (q[1:3] == 0).all() and qs[1:3].isnan().all() and y[1].isnan().sum() == 1
+        assert y[2, 3] == -float("inf") and not y[0].isnan().any()
+        h, rq, rs = ora.swiglu(ora.f64(gu[3:]))
+        assert ora.close(ora.f64(y[3:]), h, 12 * ora.U32, 2 * STEP["f32"]) <= 1
+        assert np.array_equal(q[3:].cpu().numpy(), rq) and ora.close(ora.f64(qs[3:]), rs, 13 * ora.U32) <= 1

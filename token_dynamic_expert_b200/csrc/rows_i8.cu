@@ -133,8 +133,9 @@ __device__ __forceinline__ Vec<int8_t, V> low_bytes(const uint32_t (&w)[V]) {
 // neither 0 nor infinite.
 // Relative error in half steps: ex2.approx 4, the factor 1 and its product 1,
 // 1 + e 1, rcp.approx 2, the two products 2: 11.  Above g = 128 e^-g is far
-// below half a step of 1; below g = -126 ln 2 the reciprocal underflows and
-// the result is 0.
+// below half a step of 1.  Below g = -126 ln 2 the reciprocal underflows: rows with
+// a g under kSiluLow are formed again in fp64 (low_row).
+constexpr float kSiluLow = -87.f;
 __device__ __forceinline__ F2 silu_mul(F2 g, F2 u) {
   const F2 n = two(fmaxf(-first(g), -128.f), fmaxf(-second(g), -128.f));
   const F2 y = mul2(n, two(-1.442695041f));  // -y
@@ -169,10 +170,10 @@ __device__ __forceinline__ float max_abs(float m, const float (&p)[V]) {
   return m;
 }
 
-// The same in fp64, with the same limit below; and the nearest integer of
+// The same in fp64 (-infinity counts as its limit, 0); and the nearest integer of
 // 127 w / top.  Calls, not inlined: rare, and large in registers.
 __device__ __noinline__ double silu_mul64(float g, float u) {
-  return g < -87.336545f ? 0.0 : (double)g / (1.0 + exp(-(double)g)) * (double)u;
+  return (g == -INFINITY ? -0.0 : (double)g / (1.0 + exp(-(double)g))) * (double)u;
 }
 __device__ __noinline__ int quotient64(double w, double top) {
   return __double2int_rn(w * 127.0 / top);
@@ -269,9 +270,53 @@ __device__ __noinline__ void far_row(const RowArgs& A) {
   }
 }
 
+// A row (swiglu) with a gate so far below zero that fp32 loses SiLU(g): all of its
+// outputs once more in fp64, each thread its own elements.  The other rows pay for
+// the smallest gate of a thread (65536 rows of 512: 35.2 -> 35.9 us; a thread that
+// formed such elements again on the way took 43.6).
+template <typename T, int V, bool ONE>
+__device__ __noinline__ void low_row(const RowArgs& A) {
+  __shared__ double s_max[32];
+  const int lane = threadIdx.x & 31, tid = ONE ? lane : threadIdx.x;
+  const int step = ONE ? 32 : blockDim.x;
+  const int64_t row =
+      ONE ? (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  const T* g = static_cast<const T*>(A.a) + row * A.lda;
+  auto larger = [](double a, double b) { return b <= a || a != a ? a : b; };  // NaN stays
+  double top = 0.0;
+#pragma unroll 1
+  for (int at = tid * V; at < A.d; at += step * V)
+#pragma unroll 1
+    for (int j = at; j < at + V; ++j) {
+      const double h = silu_mul64(to_f(g[j]), to_f(g[A.d + j]));
+      if (A.y != nullptr) static_cast<T*>(A.y)[row * A.ldy + j] = from_f<T>((float)h);
+      top = larger(top, fabs(h));
+    }
+  for (int o = 16; o > 0; o >>= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (!ONE) {
+    if (lane == 0) s_max[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < step / 32; ++w) top = larger(top, s_max[w]);
+  }
+  if (A.q == nullptr) return;
+  const float M = (float)top;
+  const bool usable = isfinite(M) && M >= kMinMax;
+#pragma unroll 1
+  for (int at = tid * V; at < A.d; at += step * V)
+#pragma unroll 1
+    for (int j = at; j < at + V; ++j)
+      A.q[row * A.ldq + j] =
+          usable ? (int8_t)quotient64(silu_mul64(to_f(g[j]), to_f(g[A.d + j])), top) : (int8_t)0;
+  if (tid == 0)
+    A.q_scale[row] = usable        ? (float)(top / 127.0)
+                     : isfinite(M) ? 0.f
+                                   : __uint_as_float(0x7fc00000u);
+}
+
 // ONE: a warp a row and kRowWarps rows a CTA, no barrier; else a CTA a row.
-// far_args: A once more, for far_row, which takes its address (with A's own address
-// taken the norm of 21845 rows of 768 took 36.7 us instead of 30.5).
+// far_args: A once more, for far_row and low_row, which take its address (with A's own
+// address taken the norm of 21845 rows of 768 took 36.7 us instead of 30.5).
 template <typename T, int V, int ITEMS, bool SWIGLU, bool ONE>
 __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1)
     k_rows_i8(const RowArgs A, const __grid_constant__ RowArgs far_args) {
@@ -302,7 +347,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1)
     }
   }
   float v[ITEMS][V];  // norm: s; swiglu: h
-  float ss = 0.f, mx = 0.f;
+  float ss = 0.f, mx = 0.f, low = 0.f;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int at = i * nt + tid;
@@ -314,6 +359,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1)
 #pragma unroll
       for (int c = 0; c < V; c += 2) {
         const bool pair = c + 1 < V;
+        low = fminf(low, fminf(v[i][c], pair ? v[i][c + 1] : 0.f));
         const F2 h = silu_mul(two(v[i][c], pair ? v[i][c + 1] : 0.f), two(w[c], pair ? w[c + 1] : 0.f));
         v[i][c] = first(h);
         if (pair) v[i][c + 1] = second(h);
@@ -358,7 +404,8 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1)
   // (the exact division costs SwiGLU 1 us of 36 at 65536 rows of 512)
   const float inv = !usable || far ? 0.f : SWIGLU ? quotient(127.f, M) : __fdiv_rn(127.f, M);
   const float inv_lo = inv * (1.f - kRel), inv_hi = inv * (1.f + kRel);
-  uint32_t differ = usable && far ? 1u : 0u;
+  // bit 31: a low gate (the differences of sums with kMagic leave it 0)
+  uint32_t differ = (usable && far ? 1u : 0u) | (SWIGLU && low < kSiluLow ? 0x80000000u : 0u);
 
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
@@ -388,7 +435,16 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowWarps : 1024, 1)
   }
   if (A.q != nullptr && tid == 0)
     A.q_scale[row] = usable ? (far_ss ? M : M * (r * (1.f / 127.f))) : finite ? 0.f : __uint_as_float(0x7fc00000u);
-  if (A.q != nullptr && (ONE ? __any_sync(0xffffffffu, differ != 0u) : __syncthreads_or((int)differ) != 0)) {
+  if ((SWIGLU || A.q != nullptr) &&
+      (ONE ? __any_sync(0xffffffffu, differ != 0u) : __syncthreads_or((int)differ) != 0)) {
+    if (SWIGLU) {
+      const int is_low = (int)(differ >> 31);
+      if (ONE ? __any_sync(0xffffffffu, is_low) : __syncthreads_or(is_low) != 0) {
+        low_row<T, V, ONE>(far_args);
+        return;
+      }
+      if (A.q == nullptr) return;
+    }
     // fp64: first M, from the elements that fp32 cannot tell from the largest
     if (ONE) __syncwarp();  // s_top is 0 for every lane
     const float cand = M * (1.f - 4.f * kRel);
