@@ -18,6 +18,8 @@
 // needs clearing.  Bound by latency, and by the scattered 4-byte stores.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "ace_common.cuh"
 #include "ace_internal.h"
 #include "compact.cuh"
@@ -175,19 +177,46 @@ __global__ void __launch_bounds__(kGroupThreads) k_group(const GroupArgs A) {
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether the current device can place a cluster of 16 of these CTAs, an SM each, in
+// one of its GPCs: 8 is what every device offers, and a partition of one may have no
+// more.  Asked once a device (the answer takes as long as a launch).
+bool sixteen_fit() {
+  static std::atomic<int> known[64] = {};  // 0: not asked, 1: no, 2: yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  int k = known[dev].load(std::memory_order_relaxed);
+  if (k == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kGroupThreads);
+    cfg.dynamicSmemBytes = (size_t)2 * kGroupWarps * kMaxE * sizeof(uint32_t);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 16;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    k = cudaFuncSetAttribute(k_group, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                    cudaSuccess &&
+                cudaOccupancyMaxActiveClusters(&n, k_group, &cfg) == cudaSuccess && n > 0
+            ? 2
+            : 1;
+    if (k == 1) cudaGetLastError();  // a refusal is an answer
+    known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k == 2;
+}
+
 cudaError_t launch_group(const GroupArgs& A, cudaStream_t s) {
   const size_t smem = (size_t)2 * kGroupWarps * A.E * sizeof(uint32_t);
   cudaError_t e = cudaFuncSetAttribute(k_group, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        2 * kGroupWarps * kMaxE * (int)sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   // One CTA for the chunks of a decode step; beyond it clusters, whose SMs share
-  // the scattered stores (8192 tokens of 8: 17.8 us on 8 SMs, 12.5 on 16; 512
-  // tokens: 7.7 us on 8).  16 CTAs are more than every device must offer.
-  const int nc = A.T <= kOneCta ? 1 : A.T <= kEightCtas ? 8 : 16;
-  if (nc == 16) {
-    e = cudaFuncSetAttribute(k_group, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
+  // the scattered stores (8192 tokens of 8: 16.8 us on 8 SMs, 11.3 on 16; 512
+  // tokens: 7.7 us on 8).
+  const int nc = A.T <= kOneCta ? 1 : A.T <= kEightCtas || !sixteen_fit() ? 8 : 16;
   return launch_overlapped(k_group, nc, kGroupThreads, nc, smem, s, A);
 }
 
