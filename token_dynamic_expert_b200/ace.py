@@ -32,6 +32,7 @@ ACE_SCORE_SOFTMAX, ACE_SCORE_SIGMOID = 0, 1
 SCORES = {"softmax": ACE_SCORE_SOFTMAX, "sigmoid": ACE_SCORE_SIGMOID}
 ACE_GROUP_MAX, ACE_GROUP_TOP2 = 0, 1
 GROUP_SCORES = {"max": ACE_GROUP_MAX, "top2": ACE_GROUP_TOP2}
+MAX_COUNT = 2 ** 31 - 256  # most rows, tokens or slots of one 8-bit operator
 ACE_FLAG_BAD_INDEX, ACE_FLAG_TIMEOUT, ACE_FLAG_OVERFLOW = 0x1, 0x2, 0x4
 
 _vp = ctypes.c_void_p
@@ -327,6 +328,12 @@ def _arg(t, name, dev, dtype, shape):
     return t.data_ptr()
 
 
+def check_arg(t, name, dev, dtype, shape):
+    """The checks of an optional tensor argument, for objects that keep tensors
+    for later calls."""
+    _arg(t, name, dev, dtype, shape)
+
+
 def _rows(t, name, dev, dtype, shape):
     """(address, row stride) of an optional [rows][n] tensor whose rows may lie
     apart; elements of a row are neighbours."""
@@ -416,6 +423,14 @@ def ace_moe_logits(layer, u, logits, ws, eps_rms=1e-6, stream=None):
 def _gate_opts(score, n_groups, topk_groups, group_score, renorm, scale, tau):
     return ace_gate_opts(SCORES[score], n_groups, topk_groups, GROUP_SCORES[group_score],
                          1 if renorm else 0, scale, tau)
+
+
+def check_gate(E, k, score="softmax", n_groups=1, topk_groups=1, group_score="max", renorm=True,
+               scale=1.0):
+    """Refuses options that ace_gate_topk would refuse for k of E experts."""
+    opts = _gate_opts(score, int(n_groups), int(topk_groups), group_score, bool(renorm), float(scale), 0.0)
+    _check(_lib.ace_gate_topk(None, E, ACE_F32, 0, E, k, None, opts, None, None, None, None, None),
+           "ace_gate_topk")
 
 
 def ace_gate_topk(logits, idx, weight, bias=None, score="softmax", n_groups=1, topk_groups=1,

@@ -41,9 +41,10 @@ class LayerI8:
     gamma [d] fp32; w_router [E][d] in the activations' type (bf16 or fp32); wq_gu [E][2 m][d] int8 (the
     gate rows, then the up rows) with scales s_gu [E][2 m]; wq_down [E][d][m]
     int8 with scales s_down [E][d]; bias [E] fp32 or None; factor [E] fp32 or None
-    (the ACE table of the skip rule).  d is a multiple of 64, m of 16.  gate: the
-    remaining arguments of ``ace.ace_gate_topk`` (score, n_groups, topk_groups,
-    group_score, renorm, scale)."""
+    (the ACE table of the skip rule).  d is a multiple of 64, m of 16, neither above
+    16384; E <= 512, k <= 16.  Contiguous tensors on one device, gamma and the weights
+    from 16-byte boundaries.  gate: the remaining arguments of ``ace.ace_gate_topk``
+    (score, n_groups, topk_groups, group_score, renorm, scale)."""
 
     def __init__(self, gamma, w_router, wq_gu, s_gu, wq_down, s_down, k, max_tokens, bias=None,
                  factor=None, eps=1e-6, gate=None):
@@ -55,10 +56,28 @@ class LayerI8:
             raise ValueError("d must be a multiple of 64 and m of 16, are %d and %d" % (d, m))
         if max_tokens < 1 or not 1 <= k <= E:
             raise ValueError("max_tokens must be positive and 1 <= k <= E")
+        if k > 16 or E > 512 or max(d, m) > 16384 or max_tokens * k > ace.MAX_COUNT:
+            raise ValueError("k <= 16, E <= 512, d and m <= 16384 and max_tokens * k <= %d are served" % ace.MAX_COUNT)
+        if not eps >= 0:
+            raise ValueError("eps must not be negative")
+        dev = w_router.get_device()
+        for t, name, dtype, shape in ((wq_gu, "wq_gu", torch.int8, (E, m2, d)), (s_gu, "s_gu", torch.float32, (E, m2)),
+                                      (wq_down, "wq_down", torch.int8, (E, d, m)),
+                                      (s_down, "s_down", torch.float32, (E, d)),
+                                      (bias, "bias", torch.float32, (E,)), (factor, "factor", torch.float32, (E,))):
+            if t is None and name[0] == "s":
+                raise TypeError("%s is missing" % name)
+            ace.check_arg(t, name, dev, dtype, shape)
+        for t, name in ((gamma, "gamma"), (w_router, "w_router"), (wq_gu, "wq_gu"), (wq_down, "wq_down")):
+            if t.data_ptr() % 16:
+                raise ValueError("%s must start on a 16-byte boundary" % name)
+        ace.check_gate(E, k, **(gate or {}))
         self.gamma, self.bias, self.factor, self.eps = gamma, bias, factor, float(eps)
         self.wq_gu, self.s_gu, self.wq_down, self.s_down = wq_gu, s_gu, wq_down, s_down
         self.w_router, dtype = w_router, w_router.dtype
         self.router = ace.make_router_layer(gamma, w_router)
+        if dev < 0:
+            raise ValueError("LayerI8: tensors must be on a CUDA device")
         self.E, self.d, self.m, self.k, self.max_tokens, self.dtype = E, d, m, int(k), int(max_tokens), dtype
         self.gate = dict(gate or {})
         dev, T, S = gamma.device, int(max_tokens), int(max_tokens) * int(k)
