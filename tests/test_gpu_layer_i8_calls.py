@@ -1,0 +1,90 @@
+"""Calls of one LayerI8 that share its buffers: from several streams and threads, none
+of which waits for another by itself."""
+import threading
+
+import pytest
+import torch
+
+from test_gpu_layer_i8 import GATES, _make
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(T, d, n):
+    g = torch.Generator(device="cuda").manual_seed(n + T)
+    return [torch.randn(T - i, d, generator=g, device="cuda").bfloat16() for i in range(n)]
+
+
+@pytest.mark.parametrize("T", [8, 700])
+def test_calls_on_several_streams_keep_their_results(T):
+    L, _, _ = _make(T, 512, 32, 256, 4, gate=GATES[1], bias=True)
+    us = _inputs(T, 512, 4)
+    want = [L.forward(u, torch.empty_like(u)) for u in us]
+    got = [torch.zeros_like(u) for u in us]
+    streams = [torch.cuda.Stream() for _ in us]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for u, y, s in zip(us, got, streams):
+            L.forward(u, y, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert L.status()[0] == 0
+
+
+def test_calls_from_several_threads_keep_their_results():
+    L, _, _ = _make(300, 512, 32, 256, 4)
+    us = _inputs(300, 512, 4)
+    want = [L.forward(u, torch.empty_like(u)) for u in us]
+    torch.cuda.synchronize()
+    bad, start = [], threading.Barrier(len(us))
+
+    def work(u, w):
+        s, ys = torch.cuda.Stream(), [torch.zeros_like(u) for _ in range(30)]
+        torch.cuda.current_stream().synchronize()  # ys are zeros before s writes them
+        start.wait()
+        for y in ys:
+            L.forward(u, y, stream=s)
+        s.synchronize()
+        bad.extend(i for i, y in enumerate(ys) if not torch.equal(y, w))
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(us, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_status_waits_for_a_call_on_another_stream():
+    """The status words of a call that is still running are not read too early: a bad
+    expert index cannot arise here, so the call before leaves a flag in them."""
+    from token_dynamic_expert_b200 import ace
+    L, u, _ = _make(700, 512, 32, 256, 4)
+    s, y = torch.cuda.Stream(), torch.empty_like(u)
+    for w in L.ws:
+        w.view(torch.int32)[0] = ace.ACE_FLAG_BAD_INDEX
+    torch.cuda.synchronize()
+    for _ in range(10):
+        L.forward(u, y, stream=s)
+    assert L.status() == (ace.ACE_OK, 0)
+
+
+def test_a_captured_call_between_others():
+    L, _, _ = _make(96, 512, 32, 256, 4)
+    us = _inputs(96, 512, 2)
+    want = [L.forward(u, torch.empty_like(u)) for u in us]
+    y, z = torch.zeros_like(us[0]), torch.zeros_like(us[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        L.forward(us[0], y)
+    for _ in range(3):
+        g.replay()
+        L.forward(us[1], z)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+
+
+def test_an_input_on_another_device_is_refused():
+    L, u, _ = _make(8, 128, 8, 64, 2)
+    with pytest.raises(ValueError, match="device"):
+        L.forward(u.cpu(), torch.empty(u.shape, dtype=u.dtype))

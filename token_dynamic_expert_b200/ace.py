@@ -308,6 +308,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     else lambda dev: torch.cuda.current_stream(dev).cuda_stream
 
 
+def current_raw_stream(dev):
+    """The current stream of device dev, as its handle."""
+    return _raw_stream(dev)
+
+
 def _refuse(t, name, dev, dtype, shape):
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, is %s" % (name, dtype, t.dtype))

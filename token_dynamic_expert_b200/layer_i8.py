@@ -15,12 +15,16 @@ One call runs, on the current stream and without a host synchronisation:
 
 The number of kept slots stays on the device: buffers have room for every slot,
 and the kernels stop at the last one in use.  The buffers are allocated once
-(``LayerI8(..., max_tokens)``), so a call can be captured in a CUDA graph; calls of
-one object share them and run one after the other on the device.
+(``LayerI8(..., max_tokens)``), so a call can be captured in a CUDA graph.  Calls of
+one object share them: a call waits on the device for the one before it, whichever
+stream and thread that came from.  A captured call runs when its graph is replayed;
+the program orders a replay with other replays and calls of the same object.
 Arithmetic is the operators' (see include/ace.h): integer sums are exact, int8
 rows are correctly rounded, everything else is fp32 with one rounding per stored
 result.
 """
+import threading
+
 import torch
 
 from . import ace
@@ -79,7 +83,7 @@ class LayerI8:
         if dev < 0:
             raise ValueError("LayerI8: tensors must be on a CUDA device")
         self.E, self.d, self.m, self.k, self.max_tokens, self.dtype = E, d, m, int(k), int(max_tokens), dtype
-        self.gate = dict(gate or {})
+        self.gate, self.dev = dict(gate or {}), dev
         dev, T, S = gamma.device, int(max_tokens), int(max_tokens) * int(k)
         i32, f32, i8 = (dict(dtype=t, device=dev) for t in (torch.int32, torch.float32, torch.int8))
         self.xq, self.xs = torch.empty(T, d, **i8), torch.empty(T, **f32)
@@ -96,16 +100,22 @@ class LayerI8:
             [ace.alloc_workspace(256, dev) for _ in range(3)]
         for w in self.ws:
             w.zero_()  # status() before the first call
+        self.tokens, self.views = 0, None
+        # the stream of the buffers' last use, and the end of that use
+        self.lock, self.here, self.done = threading.Lock(), torch.cuda.current_stream(dev), torch.cuda.Event()
+        self.done.record(self.here)
 
     def forward(self, u, y, residual=None, sum=None, tau=0.0, stream=None):
         """y [T][d] = the layer's output for u [T][d] (+ residual; sum, if given,
         receives u + residual, and may be either of them).  Slots but a token's
         largest are skipped where weight * factor < tau.  T <= max_tokens.  Rows of
         u and residual may lie apart; y and sum are contiguous."""
-        T, k, E = u.shape[0], self.k, self.E
+        T = u.shape[0]
         if T > self.max_tokens or u.shape[1] != self.d or u.dtype != self.dtype:
             raise ValueError("u must be [T <= %d][%d] %s" % (self.max_tokens, self.d, self.dtype))
-        if y.shape != u.shape or y.dtype != u.dtype or y.get_device() != u.get_device():
+        if u.get_device() != self.dev:
+            raise ValueError("u must be on the layer's device")
+        if y.shape != u.shape or y.dtype != u.dtype or y.get_device() != self.dev:
             raise ValueError("y must have u's shape, dtype and device")
         if not y.is_contiguous() or (sum is not None and not sum.is_contiguous()):
             raise ValueError("y and sum must be contiguous")
@@ -114,32 +124,52 @@ class LayerI8:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.forward(u, y, residual, sum, tau)
-        if u.get_device() != torch.cuda.current_device():
+        if self.dev != torch.cuda.current_device():
             with torch.cuda.device(u.device):
                 return self.forward(u, y, residual, sum, tau)
-        S = T * k
-        xq, xs, logits = self.xq[:T], self.xs[:T], self.logits[:T]
+        with self.lock:
+            if torch._C._cuda_isCurrentStreamCapturing():
+                self._enqueue(u, y, residual, sum, tau)
+                return y
+            if ace.current_raw_stream(self.dev) != self.here.cuda_stream:
+                self.here = torch.cuda.current_stream()
+                self.here.wait_event(self.done)
+            try:
+                self._enqueue(u, y, residual, sum, tau)
+            finally:
+                self.done.record(self.here)
+        return y
+
+    def _views(self, T):
+        """The buffers' parts that T tokens use."""
+        k, S = self.k, T * self.k
+        idx, weight, keep, slot_of = (t[:S].view(T, k) for t in (self.idx, self.weight, self.keep, self.slot_of))
+        return (self.xq[:T], self.xs[:T], self.logits[:T], self.sum[:T], idx, weight, keep, slot_of,
+                self.slot_token[:S], self.slot_gate[:S], self.gu[:S], self.hq[:S], self.hs[:S], self.yslot[:S],
+                self.offsets[self.E:])
+
+    def _enqueue(self, u, y, residual, sum, tau):
+        if u.shape[0] != self.tokens:  # as many as the call before: a decode loop
+            self.tokens, self.views = u.shape[0], self._views(u.shape[0])
+        xq, xs, logits, own_sum, idx, weight, keep, slot_of, slot_token, slot_gate, gu, hq, hs, yslot, n = self.views
         if sum is None and (residual is not None or not u.is_contiguous()):
-            sum = self.sum[:T]  # the router reads whole rows
-        idx, weight, keep = (t[:S].view(T, k) for t in (self.idx, self.weight, self.keep))
-        slot_of, slot_token, slot_gate = self.slot_of[:S].view(T, k), self.slot_token[:S], self.slot_gate[:S]
-        gu, hq, hs, yslot = self.gu[:S], self.hq[:S], self.hs[:S], self.yslot[:S]
+            sum = own_sum  # the router reads whole rows
         ace.ace_add_rmsnorm(u, self.gamma, residual=residual, sum=sum, q=xq, q_scale=xs, eps=self.eps)
         ace.ace_moe_logits(self.router, u if sum is None else sum, logits, self.ws[0], eps_rms=self.eps)
         ace.ace_gate_topk(logits, idx, weight, bias=self.bias, factor=self.factor, tau=tau, keep=keep,
                           **self.gate)
-        ace.ace_moe_group(idx, E, self.offsets, slot_of, keep=keep, gate=weight, slot_token=slot_token,
+        ace.ace_moe_group(idx, self.E, self.offsets, slot_of, keep=keep, gate=weight, slot_token=slot_token,
                           slot_gate=slot_gate)
         ace.ace_matmul_i8(xq, xs, self.wq_gu, self.s_gu, gu, self.ws[1], offsets=self.offsets, row_of=slot_token)
-        ace.ace_swiglu(gu, q=hq, q_scale=hs, n_valid=self.offsets[E:])
+        ace.ace_swiglu(gu, q=hq, q_scale=hs, n_valid=n)
         ace.ace_matmul_i8(hq, hs, self.wq_down, self.s_down, yslot, self.ws[2], offsets=self.offsets,
                           slot_scale=slot_gate)
         ace.ace_moe_combine(slot_of, yslot, y, self.ws[3])
-        return y
 
     def status(self, stream=None):
         """(code, flags) of the last call, the first of its steps that is not
-        ACE_OK (synchronises)."""
+        ACE_OK (synchronises; of a replay on another stream, name it)."""
         with torch.cuda.device(self.ws[0].device):
+            self.done.synchronize()
             codes = [ace.ace_read_status(w, stream) for w in self.ws]
         return next((c for c in codes if c[0] != ace.ACE_OK), codes[-1])
