@@ -88,3 +88,44 @@ def test_an_input_on_another_device_is_refused():
     L, u, _ = _make(8, 128, 8, 64, 2)
     with pytest.raises(ValueError, match="device"):
         L.forward(u.cpu(), torch.empty(u.shape, dtype=u.dtype))
+
+
+def test_rows_that_start_anywhere():
+    """u and residual off 16-byte boundaries give the bits of aligned ones; y may be
+    either of them; a y or sum of that kind, or one in the other, is refused before
+    the first kernel."""
+    L, u, res = _make(24, 256, 8, 64, 2)
+    n = u.numel()
+
+    def off(t, by):
+        b = torch.zeros(n + 64, dtype=t.dtype, device="cuda")
+        v = b[by:by + n].view(t.shape)
+        return v.copy_(t)
+
+    for by in (1, 2, 8):
+        want, got = torch.empty_like(u), torch.empty_like(u)
+        L.forward(u, want)
+        L.forward(off(u, by), got)
+        assert torch.equal(want, got)
+        L.forward(u, want, res)
+        L.forward(off(u, by), got, off(res, by + 1))
+        assert torch.equal(want, got)
+    for into in (0, 1):
+        a, b = u.clone(), res.clone()
+        L.forward(a, (a, b)[into], b)
+        assert torch.equal((a, b)[into], want)
+    both = torch.zeros(2 * n, dtype=u.dtype, device="cuda")
+    kept = res.clone()
+    for y, s in ((off(u, 1), None), (torch.empty_like(u), off(res, 1)), (both[8:8 + n].view(u.shape), both[:n].view(u.shape)),
+                 (res, res)):
+        with pytest.raises(ValueError, match="16-byte|overlap"):
+            L.forward(u, y, res, sum=s)
+    with pytest.raises(TypeError):
+        L.forward(u, torch.empty_like(u), res, sum=res, tau=None)
+    with pytest.raises(ValueError, match="must be"):
+        L.forward(u[0], torch.empty_like(u[0]), res, sum=res)
+    torch.cuda.synchronize()
+    assert torch.equal(res, kept) and not both.any()
+    y = torch.empty_like(u)
+    L.forward(u, both[n:].view(u.shape), res, sum=both[:n].view(u.shape))  # neighbours
+    assert torch.equal(both[n:].view(u.shape), want)

@@ -109,9 +109,10 @@ class LayerI8:
         """y [T][d] = the layer's output for u [T][d] (+ residual; sum, if given,
         receives u + residual, and may be either of them).  Slots but a token's
         largest are skipped where weight * factor < tau.  T <= max_tokens.  Rows of
-        u and residual may lie apart; y and sum are contiguous."""
-        T = u.shape[0]
-        if T > self.max_tokens or u.shape[1] != self.d or u.dtype != self.dtype:
+        u and residual may lie apart and start anywhere; y and sum are contiguous,
+        from 16-byte boundaries, and apart from each other; y may be u or residual."""
+        T, tau = u.shape[0], float(tau)
+        if u.dim() != 2 or T > self.max_tokens or u.shape[1] != self.d or u.dtype != self.dtype:
             raise ValueError("u must be [T <= %d][%d] %s" % (self.max_tokens, self.d, self.dtype))
         if u.get_device() != self.dev:
             raise ValueError("u must be on the layer's device")
@@ -119,6 +120,12 @@ class LayerI8:
             raise ValueError("y must have u's shape, dtype and device")
         if not y.is_contiguous() or (sum is not None and not sum.is_contiguous()):
             raise ValueError("y and sum must be contiguous")
+        if y.data_ptr() % 16 or (sum is not None and sum.data_ptr() % 16):
+            raise ValueError("y and sum must start on 16-byte boundaries")
+        if sum is not None and abs(sum.data_ptr() - y.data_ptr()) < y.numel() * y.element_size():
+            raise ValueError("y and sum overlap")
+        if stream is not None and stream.device.index != self.dev:
+            raise ValueError("stream must be on the layer's device")
         if T == 0:
             return y
         if stream is not None:
@@ -152,8 +159,8 @@ class LayerI8:
         if u.shape[0] != self.tokens:  # as many as the call before: a decode loop
             self.tokens, self.views = u.shape[0], self._views(u.shape[0])
         xq, xs, logits, own_sum, idx, weight, keep, slot_of, slot_token, slot_gate, gu, hq, hs, yslot, n = self.views
-        if sum is None and (residual is not None or not u.is_contiguous()):
-            sum = own_sum  # the router reads whole rows
+        if sum is None and (residual is not None or not u.is_contiguous() or u.data_ptr() % 16):
+            sum = own_sum  # the router reads whole rows in 16-byte vectors
         ace.ace_add_rmsnorm(u, self.gamma, residual=residual, sum=sum, q=xq, q_scale=xs, eps=self.eps)
         ace.ace_moe_logits(self.router, u if sum is None else sum, logits, self.ws[0], eps_rms=self.eps)
         ace.ace_gate_topk(logits, idx, weight, bias=self.bias, factor=self.factor, tau=tau, keep=keep,
