@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+import i8_oracle as ora
 from test_gpu_layer_i8 import GATES, _make
 
 pytestmark = pytest.mark.gpu
@@ -129,3 +130,20 @@ def test_rows_that_start_anywhere():
     y = torch.empty_like(u)
     L.forward(u, both[n:].view(u.shape), res, sum=both[:n].view(u.shape))  # neighbours
     assert torch.equal(both[n:].view(u.shape), want)
+
+
+@pytest.mark.parametrize("T", [1, 8, 200])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_router_bias_is_part_of_the_logits(T, dtype):
+    from token_dynamic_expert_b200 import layer_i8
+    L, u, _ = _make(T, 256, 32, 64, 4, dtype=dtype)
+    b = torch.randn(32, device="cuda")
+    B = layer_i8.LayerI8(L.gamma, L.w_router, L.wq_gu, L.s_gu, L.wq_down, L.s_down, 4, T, router_bias=b)
+    y = torch.empty_like(u)
+    L.forward(u, y)
+    B.forward(u, y)
+    assert torch.equal(B.logits, L.logits + b)  # the sum of the products, then one addition
+    idx, w = ora.gate(ora.f64(B.logits), 4)
+    assert (B.idx.view(T, 4).cpu().numpy() == idx).all()
+    spread = float(B.logits.max() - B.logits.min())
+    assert ora.close(ora.f64(B.weight.view(T, 4)), w, (2 * spread + 20) * ora.U32, 1e-37) <= 1

@@ -48,6 +48,7 @@ def test_sound_arguments_end_at_the_device(mod):
     (dict(gamma=torch.ones(64)), ValueError, "gamma"),
     (dict(s_gu=None), TypeError, "s_gu"), (dict(s_down=None), TypeError, "s_down"),
     (dict(bias=torch.zeros(7)), ValueError, "bias"), (dict(bias=torch.zeros(8, dtype=torch.float64)), TypeError, "bias"),
+    (dict(router_bias=torch.zeros(9)), ValueError, "router_bias"),
     (dict(factor=torch.zeros(16)[::2]), ValueError, "factor"),
     (dict(wq_gu="off"), ValueError, "wq_gu must start"), (dict(wq_down="off"), ValueError, "wq_down must start"),
     (dict(w_router="off"), ValueError, "w_router must start"), (dict(gamma="off"), ValueError, "gamma must start"),

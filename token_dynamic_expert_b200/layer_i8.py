@@ -45,13 +45,14 @@ class LayerI8:
     gamma [d] fp32; w_router [E][d] in the activations' type (bf16 or fp32); wq_gu [E][2 m][d] int8 (the
     gate rows, then the up rows) with scales s_gu [E][2 m]; wq_down [E][d][m]
     int8 with scales s_down [E][d]; bias [E] fp32 or None; factor [E] fp32 or None
-    (the ACE table of the skip rule).  d is a multiple of 64, m of 16, neither above
+    (the ACE table of the skip rule); router_bias [E] fp32 or None, part of the logits
+    (bias takes part in the choice alone).  d is a multiple of 64, m of 16, neither above
     16384; E <= 512, k <= 16.  Contiguous tensors on one device, gamma and the weights
     from 16-byte boundaries.  gate: the remaining arguments of ``ace.ace_gate_topk``
     (score, n_groups, topk_groups, group_score, renorm, scale)."""
 
     def __init__(self, gamma, w_router, wq_gu, s_gu, wq_down, s_down, k, max_tokens, bias=None,
-                 factor=None, eps=1e-6, gate=None):
+                 factor=None, eps=1e-6, gate=None, router_bias=None):
         E, m2, d = wq_gu.shape
         m = m2 // 2
         if m2 % 2 or tuple(wq_down.shape) != (E, d, m) or tuple(w_router.shape) != (E, d):
@@ -68,7 +69,8 @@ class LayerI8:
         for t, name, dtype, shape in ((wq_gu, "wq_gu", torch.int8, (E, m2, d)), (s_gu, "s_gu", torch.float32, (E, m2)),
                                       (wq_down, "wq_down", torch.int8, (E, d, m)),
                                       (s_down, "s_down", torch.float32, (E, d)),
-                                      (bias, "bias", torch.float32, (E,)), (factor, "factor", torch.float32, (E,))):
+                                      (bias, "bias", torch.float32, (E,)), (factor, "factor", torch.float32, (E,)),
+                                      (router_bias, "router_bias", torch.float32, (E,))):
             if t is None and name[0] == "s":
                 raise TypeError("%s is missing" % name)
             ace.check_arg(t, name, dev, dtype, shape)
@@ -78,8 +80,8 @@ class LayerI8:
         ace.check_gate(E, k, **(gate or {}))
         self.gamma, self.bias, self.factor, self.eps = gamma, bias, factor, float(eps)
         self.wq_gu, self.s_gu, self.wq_down, self.s_down = wq_gu, s_gu, wq_down, s_down
-        self.w_router, dtype = w_router, w_router.dtype
-        self.router = ace.make_router_layer(gamma, w_router)
+        self.w_router, self.router_bias, dtype = w_router, router_bias, w_router.dtype
+        self.router = ace.make_router_layer(gamma, w_router, router_bias)
         if dev < 0:
             raise ValueError("LayerI8: tensors must be on a CUDA device")
         self.E, self.d, self.m, self.k, self.max_tokens, self.dtype = E, d, m, int(k), int(max_tokens), dtype
