@@ -333,6 +333,12 @@ def _arg(t, name, dev, dtype, shape):
     return t.data_ptr()
 
 
+def _fits(name, a, b):
+    """Refuses counts beyond the operators' (a C int would take their low bits)."""
+    if a > MAX_COUNT or b > MAX_COUNT:
+        raise AceError(ACE_ERR_UNSUPPORTED, "%s of %d x %d" % (name, a, b))
+
+
 def check_arg(t, name, dev, dtype, shape):
     """The checks of an optional tensor argument, for objects that keep tensors
     for later calls."""
@@ -347,6 +353,7 @@ def _rows(t, name, dev, dtype, shape):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(t, name, dev, dtype, shape)
     rows, n = shape
+    _fits(name, rows, n)
     ld, step = t.stride()
     if (n > 1 and step != 1) or (rows > 1 and ld < n):
         raise ValueError("%s must have rows of neighbouring elements" % name)
@@ -415,6 +422,7 @@ def ace_moe_logits(layer, u, logits, ws, eps_rms=1e-6, stream=None):
     if u.dim() != 2 or u.shape[1] != layer.d or _dtype_code(u) != layer.dtype:
         raise ValueError("u must be [T][%d] in the layer's dtype" % layer.d)
     T = u.shape[0]
+    _fits("u", T, 1)
     if ws.get_device() != dev:
         raise ValueError("tensors are on several devices: ws is not on device %d" % dev)
     _run(_lib.ace_moe_logits, "ace_moe_logits", dev, stream, layer,
@@ -448,6 +456,7 @@ def ace_gate_topk(logits, idx, weight, bias=None, score="softmax", n_groups=1, t
         raise ValueError("logits must be [T][E] and idx [T][k]")
     T, E = logits.shape
     k, dev = idx.shape[1], logits.get_device()
+    _fits("idx", T, k)
     pl, ld = _rows(logits, "logits", dev, logits.dtype, (T, E))
     opts = _gate_opts(score, int(n_groups), int(topk_groups), group_score, bool(renorm), float(scale),
                       float(tau))
@@ -468,6 +477,8 @@ def ace_moe_group(idx, E, offsets, slot_of, keep=None, gate=None, slot_token=Non
         raise ValueError("idx must be [T][k]")
     shape, dev = idx.shape, idx.get_device()
     T, k = shape
+    _fits("idx", T, k)
+    _fits("offsets", E, 1)
     _run(_lib.ace_moe_group, "ace_moe_group", dev, stream, _arg(idx, "idx", dev, torch.int32, shape),
          _arg(keep, "keep", dev, torch.uint8, shape), _arg(gate, "gate", dev, torch.float32, shape), T, k,
          E, _arg(offsets, "offsets", dev, torch.int32, (E + 1,)),
@@ -495,6 +506,7 @@ def ace_matmul_i8(xq, x_scale, wq, w_scale, out, ws, offsets=None, row_of=None, 
     if E != 1 and offsets is None:
         raise ValueError("wq of several experts needs offsets")
     N, K = wshape[-2:]
+    _fits("wq", E, N)
     n, S = xq.shape[0], out.shape[0]
     px, ldx = _rows(xq, "xq", dev, torch.int8, (n, K))
     po, ldo = _rows(out, "out", dev, out.dtype, (S, N))
