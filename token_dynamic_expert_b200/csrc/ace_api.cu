@@ -510,14 +510,19 @@ ace_status ace_moe_logits(const ace_layer* layer, const void* u, int T, float ep
   const ace_status st = check_common(layer, u, T, &o, ws, false);
   if (st != ACE_OK) return st;
   if (!(eps_rms >= 0.f) || (T > 0 && (!logits || !aligned(logits, 4)))) return ACE_ERR_INVALID_ARG;
-  const ByteSpan out(logits, layer->E, T, layer->E, 4);
-  if (out.meets(ByteSpan(u, layer->d, T, layer->d, esize(layer->dtype))) ||
-      out.meets(ByteSpan(ws, 1, (int64_t)ws_bytes, 1, 1)))
-    return ACE_ERR_INVALID_ARG;
   const ace_layer& L = *layer;
   const int num_sms = device_sm_count();
   const FwdLayout ly = fwd_layout(L, T, num_sms);
   if (ws_bytes < ly.idx) return ACE_ERR_WORKSPACE;
+  // the logits and the part of ws in use are written, the rest is read
+  const size_t es = esize(L.dtype);
+  const ByteSpan out(logits, L.E, T, L.E, 4), scratch(ws, 1, (int64_t)ly.idx, 1, 1);
+  const ByteSpan in[4] = {ByteSpan(u, L.d, T, L.d, es), ByteSpan(L.gamma, 1, L.d, 1, 4),
+                          ByteSpan(L.w_router, L.d, L.E, L.d, es),
+                          ByteSpan(L.router_bias, 1, L.E, 1, 4)};
+  for (const ByteSpan& i : in)
+    if (out.meets(i) || scratch.meets(i)) return ACE_ERR_INVALID_ARG;
+  if (out.meets(scratch)) return ACE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const StatusClear clr = status_clear(ly, ws, false);
   if (T == 0) {

@@ -661,14 +661,18 @@ ace_status ace_matmul_i8(const ace_i8_product* p, int S, void* out, int64_t ldo,
     return ACE_ERR_INVALID_ARG;
   if (p->ldx < p->K || p->ldx % 16 != 0 || ldo < p->N) return ACE_ERR_INVALID_ARG;
   const int64_t EN = (int64_t)p->E * p->N;
-  const ByteSpan o(out, ldo, S, p->N, es);
-  if (o.meets(ByteSpan(p->xq, p->ldx, p->n_rows, p->K, 1)) ||
-      o.meets(ByteSpan(p->wq, p->K, EN, p->K, 1)) ||
-      o.meets(ByteSpan(p->x_scale, 1, p->n_rows, 1, 4)) ||
-      o.meets(ByteSpan(p->w_scale, 1, EN, 1, 4)) ||
-      o.meets(ByteSpan(p->slot_scale, 1, S, 1, 4)) || o.meets(ByteSpan(p->row_of, 1, S, 1, 4)) ||
-      o.meets(ByteSpan(p->offsets, 1, p->E + 1, 1, 4)) || o.meets(ByteSpan(ws, 1, 256, 1, 1)))
-    return ACE_ERR_INVALID_ARG;
+  // the output and the status word are written, the rest is read
+  const ByteSpan o(out, ldo, S, p->N, es), status(ws, 1, 256, 1, 1);
+  const ByteSpan in[7] = {ByteSpan(p->xq, p->ldx, p->n_rows, p->K, 1),
+                          ByteSpan(p->wq, p->K, EN, p->K, 1),
+                          ByteSpan(p->x_scale, 1, p->n_rows, 1, 4),
+                          ByteSpan(p->w_scale, 1, EN, 1, 4),
+                          ByteSpan(p->slot_scale, 1, S, 1, 4),
+                          ByteSpan(p->row_of, 1, S, 1, 4),
+                          ByteSpan(p->offsets, 1, p->E + 1, 1, 4)};
+  for (const ByteSpan& i : in)
+    if (o.meets(i) || status.meets(i)) return ACE_ERR_INVALID_ARG;
+  if (o.meets(status)) return ACE_ERR_INVALID_ARG;
   MatArgs A;
   A.x_scale = p->x_scale;
   A.w_scale = p->w_scale;
