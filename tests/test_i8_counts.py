@@ -46,3 +46,11 @@ def test_counts_beyond_32_bits(ace, n):
         with pytest.raises(ace.AceError) as e:
             call()
         assert e.value.code == ace.ACE_ERR_UNSUPPORTED, i
+
+
+def test_logits_of_more_tokens_than_the_limit(ace):
+    import ctypes
+    L = ace.ace_layer(d=64, E=8, m=64, k=1, dtype=1, gamma=0x3000000, w_router=0x3000000)
+    for n in (2 ** 31 - 255, 2 ** 31 - 1):
+        assert ace.lib().ace_moe_logits(ctypes.byref(L), 0x1000000, n, 1e-6, 0x2000000, 0xA000000, 1 << 30,
+                                        None) == ace.ACE_ERR_UNSUPPORTED

@@ -510,6 +510,7 @@ ace_status ace_moe_logits(const ace_layer* layer, const void* u, int T, float ep
   const ace_status st = check_common(layer, u, T, &o, ws, false);
   if (st != ACE_OK) return st;
   if (!(eps_rms >= 0.f) || (T > 0 && (!logits || !aligned(logits, 4)))) return ACE_ERR_INVALID_ARG;
+  if (T > kMaxCount) return ACE_ERR_UNSUPPORTED;
   const ace_layer& L = *layer;
   const int num_sms = device_sm_count();
   const FwdLayout ly = fwd_layout(L, T, num_sms);
