@@ -17,7 +17,7 @@
 // largest first) and leaves the list in shared memory; each of the k rounds takes
 // the largest of the lanes' heads by redux.max and moves one lane on.  Bound by
 // instruction issue (about 1050 a token) and the latency of the rounds; the data
-// are 8.9 MB at 8192 tokens of 256 experts: 14.7 us with a bias and 8 groups, 10.2
+// are 8.9 MB at 8192 tokens of 256 experts: 14.9 us with a bias and 8 groups, 10.7
 // without; one token 2.5 us.  Lists kept in registers and shifted, with 64-bit
 // scores throughout the ties, took 43 us.
 //

@@ -28,7 +28,7 @@
 //   warps 10-17  with row_of: four slot rows an instruction (tile::gather4).  A
 //                warp issues these one thread at a time, about 75 cycles each, so
 //                several warps share them (65536 gathered rows, 256 x 1024 x 2048:
-//                1, 4, 8 warps 591, 180, 172 us)
+//                2, 4, 8 warps 258, 205, 199 us, call after call)
 // Two TMEM accumulators alternate between items, so an epilogue overlaps the
 // next main loop.  All waits are bounded.
 // A gather warp without rows in an item passes it over, and begins an item only

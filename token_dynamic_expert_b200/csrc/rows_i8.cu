@@ -10,15 +10,15 @@
 //
 // One pass over the data: a row's elements stay in registers between the
 // statistics and the outputs.  Few rows are bound by latency (launch, one load, two
-// barriers: 2.1 us for one row of 2048); many by HBM and, just before it, by
-// instruction issue (norm of 8191 rows of 2048 with residual, y and int8 28 us, 5.4
-// TB/s; SwiGLU of 65536 rows of 512 35 us, 4.8 TB/s).
+// barriers: 2.0 us for one row of 2048); many by HBM and, just before it, by
+// instruction issue (norm of 8191 rows of 2048 with residual, y and int8 28.7 us, 5.3
+// TB/s; SwiGLU of 65536 rows of 512 36 us, 4.7 TB/s).
 //
 // Rounding of q.  127 p / M is formed in fp32 with a relative error of at most
 // kRel (counted below), which misplaces about one element in 50000 next to a
 // half.  Elements whose interval q (1 -+ kRel) straddles a half are settled in
 // fp64 from the stored inputs, with M in fp64 too, so q is the correctly
-// rounded quotient; about one row of 2048 in twenty-five has such an element.
+// rounded quotient; about one norm row of 2048 in thirty has such an element.
 #include <math.h>
 #include <string.h>
 
