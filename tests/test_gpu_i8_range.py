@@ -69,6 +69,26 @@ def test_norm_residual_and_in_place_beyond_the_range():
         assert torch.equal(x, want["y"]) and torch.equal(res, want["sum"])
 
 
+@pytest.mark.parametrize("T,d", [(3, 64), (700, 512), (700, 2048), (3, 1001)])
+def test_norm_outputs_alone_beyond_the_range(T, d):
+    """Every subset of the outputs has the bits of all of them together."""
+    from token_dynamic_expert_b200 import ace
+    g = torch.Generator(device="cuda").manual_seed(d)
+    gamma = torch.rand(d, generator=g, device="cuda") + 0.5
+    size = torch.tensor([1e21, 1.0, 1e-24], device="cuda")[torch.arange(T, device="cuda") % 3][:, None]
+    for dt in (torch.bfloat16, torch.float32):
+        x, res = ((torch.randn(T, d, generator=g, device="cuda") * size).to(dt) for _ in range(2))
+        for r in (None, res):
+            want = _norm(x, gamma, 0.0, r)
+            for names in (("y",), ("sum", "y"), ("q", "q_scale"), ("y", "q", "q_scale"), ("sum", "q", "q_scale")):
+                o = {n: torch.empty_like(want[n]) for n in names}
+                ace.ace_add_rmsnorm(x, gamma, residual=r, eps=0.0, **o)
+                assert all(torch.equal(o[n], want[n]) for n in names), names
+            a, b = x.clone(), res.clone()  # y over either input, the sum not kept
+            ace.ace_add_rmsnorm(a, gamma, residual=None if r is None else b, eps=0.0, y=a if r is None else b)
+            assert torch.equal(a if r is None else b, want["y"])
+
+
 def test_norm_of_zero_rows_without_eps():
     """0 / 0, as the formula has it, in y; the int8 row is zeros."""
     x = torch.zeros(3, 256, device="cuda")

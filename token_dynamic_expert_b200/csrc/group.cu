@@ -217,6 +217,10 @@ cudaError_t launch_group(const GroupArgs& A, cudaStream_t s) {
   // the scattered stores (8192 tokens of 8: 16.8 us on 8 SMs, 11.3 on 16; 512
   // tokens: 7.7 us on 8).
   const int nc = A.T <= kOneCta ? 1 : A.T <= kEightCtas || !sixteen_fit() ? 8 : 16;
+  if (nc == 16) {
+    e = cudaFuncSetAttribute(k_group, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   return launch_overlapped(k_group, nc, kGroupThreads, nc, smem, s, A);
 }
 
