@@ -590,7 +590,7 @@ typedef struct {
  *   element.  offsets rise from 0 to at most S; rows of out from offsets[E] on
  *   are left as they were (their number may be known to the device alone).
  *   Offsets that do not raise ACE_FLAG_BAD_INDEX and nothing is computed.  A
- *   row_of outside 0 .. n_rows - 1 gives a row of zeros.  xq and wq 16-byte
+ *   row_of outside 0 .. n_rows - 1 counts as a row of zeros.  xq and wq 16-byte
  *   aligned, K a multiple of 16 up to 65536, E <= 512, any N >= 1.
  *   ws: at least 256 bytes, its status word (ace_read_status).
  * ---------------------------------------------------------------------- */

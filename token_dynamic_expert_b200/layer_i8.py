@@ -137,7 +137,7 @@ class LayerI8:
             with torch.cuda.device(u.device):
                 return self.forward(u, y, residual, sum, tau)
         with self.lock:
-            if torch._C._cuda_isCurrentStreamCapturing():
+            if torch.cuda.is_current_stream_capturing():
                 self._enqueue(u, y, residual, sum, tau)
                 return y
             if ace.current_raw_stream(self.dev) != self.here.cuda_stream:
