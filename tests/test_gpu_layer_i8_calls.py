@@ -147,3 +147,15 @@ def test_router_bias_is_part_of_the_logits(T, dtype):
     assert (B.idx.view(T, 4).cpu().numpy() == idx).all()
     spread = float(B.logits.max() - B.logits.min())
     assert ora.close(ora.f64(B.weight.view(T, 4)), w, (2 * spread + 20) * ora.U32, 1e-37) <= 1
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
+def test_a_layer_on_another_device_than_the_current_one():
+    from token_dynamic_expert_b200 import layer_i8
+    for T in (8, 96):
+        L, u, _ = _make(T, 256, 16, 64, 4)
+        want = L.forward(u, torch.empty_like(u))
+        M = layer_i8.LayerI8(*(t.to("cuda:1") for t in (L.gamma, L.w_router, L.wq_gu, L.s_gu, L.wq_down, L.s_down)), 4, T)
+        v = u.to("cuda:1")
+        got = M.forward(v, torch.empty_like(v))
+        assert M.status()[0] == 0 and torch.equal(got.cpu(), want.cpu())

@@ -261,13 +261,10 @@ cudaError_t launch_router_tc(const void* u, const float* inv_rms, const void* w3
   if (!rmap(&ma, u, (uint64_t)T, (uint64_t)d, rBM) ||
       !rmap(&mb, w3, (uint64_t)3 * E, (uint64_t)d, rBN))
     return cudaErrorInvalidValue;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e =
-        cudaFuncSetAttribute(k_router_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, rSmem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  // of the current device alone, so with every launch
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_router_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, rSmem);
+  if (e != cudaSuccess) return e;
   const int items = cdiv(T, rBM) * cdiv(E, rBN) * splits;
   const int grid = items < num_sms ? items : num_sms;
   k_router_tc<<<grid, rThreads, rSmem, s>>>(ma, mb, inv_rms, T, d, E, splits, part, status);
